@@ -1,4 +1,4 @@
-"""ctypes view of libbcg (include/bcg.h).  Loading fails loudly if the
+"""ctypes view of libbcg (include/bcg.h, include/bcg_decode.h).  Loading fails loudly if the
 library has not been built: there is no fallback implementation."""
 from __future__ import annotations
 
@@ -9,7 +9,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbcg.so")
 
 BCG_OK, BCG_EINVAL, BCG_ESHAPE, BCG_EDTYPE, BCG_EHIP = 0, -1, -2, -3, -4
-BCG_F32, BCG_BF16 = 0, 1
+BCG_F32, BCG_BF16, BCG_E4M3 = 0, 1, 2
 BCG_EULER, BCG_HEUN = 0, 1
 BCG_SCHED_LOGLINEAR = 0
 BCG_CACHE_KEEP, BCG_CACHE_STREAM = 0, 1
@@ -34,6 +34,11 @@ EXPORTS = ["bcg_last_error", "bcg_abi_version", "sigma_schedule", "sigma_crop", 
            "guided_step_dplan_static", "guided_step_rows",
            "guided_step_rows_dplan",
            "bcg_loop_create", "bcg_loop_run", "bcg_loop_last_run", "bcg_loop_destroy", "weight_patch"]
+
+# Every symbol of the second header (include/bcg_decode.h).
+DECODE_EXPORTS = ["attention_workspace_size", "paged_attention", "prompt_attention", "cache_append",
+                  "cache_workspace_size", "cache_extend", "cache_fork", "cache_free", "cache_compact",
+                  "cache_copy", "guided_logits"]
 
 vp, i32p, i64p, f32p, f64p = (C.c_void_p, C.POINTER(C.c_int32), C.POINTER(C.c_int64),
                               C.POINTER(C.c_float), C.POINTER(C.c_double))
@@ -117,6 +122,40 @@ class LoopDesc(C.Structure):
                 ("join_front", C.c_int32)]
 
 
+class AttnArgs(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("rows", "tokens", "q_heads", "kv_heads", "head_dim", "page_size",
+                                         "max_blocks", "num_pages", "q_dtype", "kv_dtype", "max_len", "max_new",
+                                         "window", "sinks")] + \
+               [("scale", C.c_float), ("reserved", C.c_int32), ("q_stride", C.c_int64),
+                ("k_page_stride", C.c_int64), ("v_page_stride", C.c_int64)] + \
+               [(n, vp) for n in ("q", "k_cache", "v_cache", "block_table", "kv_len", "q_offset", "k_scale",
+                                  "v_scale", "out", "lse", "workspace")] + [("workspace_bytes", C.c_size_t)]
+
+
+class AppendArgs(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("rows", "tokens", "kv_heads", "head_dim", "page_size", "max_blocks",
+                                         "num_pages", "dtype", "kv_dtype", "reserved")] + \
+               [(n, C.c_int64) for n in ("k_stride", "v_stride", "k_page_stride", "v_page_stride")] + \
+               [(n, vp) for n in ("k", "v", "offset", "block_table", "kv_len", "k_scale", "v_scale", "k_cache",
+                                  "v_cache")]
+
+
+class Cache(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("planes", "num_pages", "page_size", "rows", "max_blocks", "reserved")] + \
+               [(n, C.c_int64) for n in ("plane_stride", "page_stride", "page_bytes")] + \
+               [(n, vp) for n in ("pool", "block_table", "kv_len", "refs", "workspace")] + \
+               [("workspace_bytes", C.c_size_t)]
+
+
+class LogitsArgs(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n", "vocab", "logit_rows", "dtype", "out_dtype", "max_history",
+                                         "num_biases", "mask_words")] + \
+               [("logit_stride", C.c_int64), ("out_stride", C.c_int64)] + \
+               [(n, vp) for n in ("logits", "out", "cond_row", "uncond_row", "scale", "history", "history_len",
+                                  "prompt_len", "repetition", "presence", "frequency", "bias_ids", "bias",
+                                  "temperature", "mask")]
+
+
 _lib = None
 
 
@@ -147,6 +186,17 @@ def _signatures():
         "bcg_loop_destroy": ([vp], C.c_int),
         "bcg_loop_last_run": ([vp, C.POINTER(C.c_int32), C.POINTER(C.c_int32)], C.c_int),
         "weight_patch": ([C.POINTER(WeightArgs), vp], C.c_int),
+        "attention_workspace_size": ([C.c_int] * 3, C.c_size_t),
+        "paged_attention": ([C.POINTER(AttnArgs), vp], C.c_int),
+        "prompt_attention": ([C.POINTER(AttnArgs), vp], C.c_int),
+        "cache_append": ([C.POINTER(AppendArgs), vp], C.c_int),
+        "cache_workspace_size": ([C.c_int] * 3, C.c_size_t),
+        "cache_extend": ([C.POINTER(Cache), C.c_int, vp, vp, vp, vp], C.c_int),
+        "cache_fork": ([C.POINTER(Cache), C.c_int, vp, vp, vp, vp], C.c_int),
+        "cache_free": ([C.POINTER(Cache), C.c_int, vp, C.c_int, C.c_int, vp], C.c_int),
+        "cache_compact": ([C.POINTER(Cache), vp, vp, vp, vp], C.c_int),
+        "cache_copy": ([C.POINTER(Cache), C.c_int, vp, vp, vp], C.c_int),
+        "guided_logits": ([C.POINTER(LogitsArgs), vp], C.c_int),
     }
 
 
@@ -172,7 +222,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"libbcg.so not found at {LIB_PATH}; build it with "
                                "`python -m bucketed_classifier_free_amd.build`")
-        _lib = configure(C.CDLL(LIB_PATH), EXPORTS)
+        _lib = configure(C.CDLL(LIB_PATH), EXPORTS + DECODE_EXPORTS)
     return _lib
 
 

@@ -25,7 +25,9 @@ LIB = os.path.join(PKG, "libbcg.so")
 
 SOURCES = ["bcg_host.cpp", "bcg_api.hip", "bcg_loop.hip", "bcg_step_f32.hip", "bcg_step_bf16.hip",
            "bcg_step_f32_nt.hip", "bcg_step_bf16_nt.hip", "bcg_step_f32_queue.hip", "bcg_step_bf16_queue.hip",
-           "bcg_rows_f32.hip", "bcg_rows_bf16.hip", "bcg_weight.hip"]
+           "bcg_rows_f32.hip", "bcg_rows_bf16.hip", "bcg_weight.hip",
+           "bcg_attn.hip", "bcg_attn_bf16.hip", "bcg_attn_e4m3.hip", "bcg_attn_f32.hip", "bcg_cache.hip",
+           "bcg_logits.hip"]
 ARCH = "gfx950"
 
 

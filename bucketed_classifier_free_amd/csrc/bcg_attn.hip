@@ -1,0 +1,143 @@
+// paged_attention and prompt_attention: argument checks and launch shapes.
+#include <cmath>
+
+#include "bcg_attn.h"
+#include "bcg_launch.h"
+
+namespace bcg {
+
+typedef uint16_t bf16_t;
+extern template hipError_t launch_decode<bf16_t, bf16_t>(const AttnParams&, hipStream_t);
+extern template hipError_t launch_decode<bf16_t, e4m3_t>(const AttnParams&, hipStream_t);
+extern template hipError_t launch_decode<float, float>(const AttnParams&, hipStream_t);
+extern template hipError_t launch_prompt<bf16_t, bf16_t>(const AttnParams&, hipStream_t);
+extern template hipError_t launch_prompt<bf16_t, e4m3_t>(const AttnParams&, hipStream_t);
+extern template hipError_t launch_prompt<float, float>(const AttnParams&, hipStream_t);
+
+namespace {
+
+// Workgroups that a decode launch aims at when it splits the rows' tokens (8
+// a CU: rows of unlike lengths even out), and a prompt launch (2 a CU).
+constexpr int64_t kDecodeGroups = 2048, kPromptGroups = 512;
+// A split is at least this many blocks (decode: 32 tokens, prompt: 64).
+constexpr int64_t kMinBlocks = 4;
+
+// (query, head) entries of all splits: splits > 1 only while the groups of one
+// split are below the aim, and a group holds at most 16 (decode) or 128
+// (prompt) entries, so splits * entries < 2 * aim * group.
+int64_t max_parts(int64_t entries) {
+    const int64_t cap = 2 * kPromptGroups * 128;
+    static_assert(2 * kPromptGroups * 128 >= 2 * kDecodeGroups * 16, "");
+    return entries * kDecodeGroups < cap ? entries * kDecodeGroups : cap;
+}
+
+int check(const bcg_attn_args* a, const char* who, bool prompt) {
+    if (!a) return fail(BCG_EINVAL, "%s: args is NULL", who);
+    if (a->rows < 0 || a->tokens < 0 || a->tokens > (1 << 24)) return fail(BCG_ESHAPE, "%s: rows %d, tokens %d", who, a->rows, a->tokens);
+    if (!prompt && a->rows != a->tokens) return fail(BCG_ESHAPE, "%s: %d rows but %d tokens", who, a->rows, a->tokens);
+    if (a->kv_heads < 1 || a->q_heads < 1 || a->q_heads % a->kv_heads != 0 || a->q_heads > 4096)
+        return fail(BCG_ESHAPE, "%s: %d query heads over %d kv heads", who, a->q_heads, a->kv_heads);
+    if ((a->q_dtype != BCG_F32 && a->q_dtype != BCG_BF16) ||
+        (a->kv_dtype != a->q_dtype && !(a->kv_dtype == BCG_E4M3 && a->q_dtype == BCG_BF16)))
+        return fail(BCG_EDTYPE, "%s: queries of type %d over a cache of type %d", who, a->q_dtype, a->kv_dtype);
+    const int unit = a->kv_dtype == BCG_E4M3 ? 16 : 8;
+    if (a->head_dim < unit || a->head_dim > BCG_MAX_HEAD_DIM || a->head_dim % unit != 0)
+        return fail(BCG_ESHAPE, "%s: head_dim %d is not a multiple of %d up to %d", who, a->head_dim, unit, BCG_MAX_HEAD_DIM);
+    if (a->page_size < 16 || a->page_size > BCG_MAX_PAGE_SIZE || a->page_size % 16 != 0)
+        return fail(BCG_ESHAPE, "%s: page_size %d is not a multiple of 16 up to %d", who, a->page_size, BCG_MAX_PAGE_SIZE);
+    if (a->max_blocks < 0 || (int64_t)a->max_blocks * a->page_size > (1 << 30) || a->num_pages < 0)
+        return fail(BCG_ESHAPE, "%s: %d blocks of %d tokens, %d pages", who, a->max_blocks, a->page_size, a->num_pages);
+    if (a->max_len < 0 || (int64_t)a->max_len > (int64_t)a->max_blocks * a->page_size)
+        return fail(BCG_ESHAPE, "%s: max_len %d beyond the table's %d blocks of %d", who, a->max_len, a->max_blocks, a->page_size);
+    if (prompt && (a->max_new < 0 || a->max_new > a->tokens)) return fail(BCG_ESHAPE, "%s: max_new %d of %d tokens", who, a->max_new, a->tokens);
+    if ((int64_t)a->tokens * a->q_heads > INT32_MAX) return fail(BCG_ESHAPE, "%s: %d tokens of %d heads", who, a->tokens, a->q_heads);
+    if (a->window < 0 || a->sinks < 0) return fail(BCG_EINVAL, "%s: window %d, sinks %d", who, a->window, a->sinks);
+    if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return fail(BCG_EINVAL, "%s: scale %g", who, a->scale);
+    if (a->tokens == 0 || a->rows == 0) return BCG_OK;
+    const int64_t qs = (int64_t)elem_size(a->q_dtype), cs = a->kv_dtype == BCG_E4M3 ? 1 : qs;
+    const int64_t page = (int64_t)a->kv_heads * a->page_size * a->head_dim;
+    if (!a->q || !a->block_table || !a->kv_len || !a->out || (prompt && !a->q_offset)) return fail(BCG_EINVAL, "%s: NULL device pointer", who);
+    if (a->max_len > 0 && (!a->k_cache || !a->v_cache || a->num_pages < 1)) return fail(BCG_EINVAL, "%s: no cache", who);
+    if (a->kv_dtype == BCG_E4M3 && (!a->k_scale || !a->v_scale)) return fail(BCG_EINVAL, "%s: an e4m3 cache needs its scales", who);
+    if (a->kv_dtype != BCG_E4M3 && (a->k_scale || a->v_scale)) return fail(BCG_EINVAL, "%s: scales are those of an e4m3 cache", who);
+    if (a->q_stride < (int64_t)a->q_heads * a->head_dim) return fail(BCG_ESHAPE, "%s: q_stride %lld", who, (long long)a->q_stride);
+    if (a->k_page_stride < page || a->v_page_stride < page)
+        return fail(BCG_ESHAPE, "%s: page strides %lld, %lld below a page's %lld", who, (long long)a->k_page_stride,
+                    (long long)a->v_page_stride, (long long)page);
+    if (!aligned16(a->q) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || !aligned16(a->out) || a->q_stride * qs % 16 ||
+        a->k_page_stride * cs % 16 || a->v_page_stride * cs % 16)
+        return fail(BCG_EINVAL, "%s: q, its rows, the cache, its pages and out must be 16-byte aligned", who);
+    const size_t need = attention_workspace_size(a->tokens, a->q_heads, a->head_dim);
+    if (!a->workspace || a->workspace_bytes < need || !aligned16(a->workspace))
+        return fail(BCG_EINVAL, "%s: a workspace of %zu bytes is needed, 16-byte aligned (%zu given)", who, need, a->workspace_bytes);
+    const size_t ob = (size_t)a->tokens * a->q_heads * a->head_dim * qs;
+    const size_t qb = ((size_t)(a->tokens - 1) * a->q_stride + (size_t)a->q_heads * a->head_dim) * qs;
+    if (any_overlap(a->q, qb, a->out, ob) || any_overlap(a->workspace, need, a->out, ob)) return fail(BCG_EINVAL, "%s: out overlaps q or the workspace", who);
+    return BCG_OK;
+}
+
+int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
+    clear_error();
+    const int rc = check(a, who, prompt);
+    if (rc != BCG_OK) return rc;
+    if (a->tokens == 0 || a->rows == 0 || (prompt && a->max_new == 0)) return BCG_OK;
+    AttnParams p{};
+    p.q = a->q; p.k = a->k_cache; p.v = a->v_cache;
+    p.table = a->block_table; p.len = a->kv_len; p.qoff = prompt ? a->q_offset : nullptr;
+    p.kscale = a->k_scale; p.vscale = a->v_scale; p.out = a->out; p.lse = a->lse;
+    p.qstride = a->q_stride; p.kps = a->k_page_stride; p.vps = a->v_page_stride;
+    p.rows = a->rows; p.tokens = a->tokens; p.qh = a->q_heads; p.kvh = a->kv_heads;
+    p.G = a->q_heads / a->kv_heads; p.D = a->head_dim; p.ps = a->page_size; p.maxb = a->max_blocks; p.np = a->num_pages;
+    p.shift = (a->page_size & (a->page_size - 1)) == 0 ? __builtin_ctz(a->page_size) : -1;
+    p.window = a->window; p.sinks = a->window > 0 ? a->sinks : 0; p.max_len = a->max_len;
+    p.max_new = a->max_new;
+    p.scale2 = a->scale * 1.4426950408889634f;
+    const int T = prompt ? 64 : 32, C = prompt ? prompt_columns(a->q_dtype, a->head_dim) : 16;
+    const int64_t cols = prompt ? (int64_t)a->max_new * p.G : p.G;
+    p.tiles = (int)((cols + C - 1) / C);
+    // blocks of the longest list (visible_blocks): all of max_len, or the sinks' and the window's
+    int64_t nb = ((int64_t)a->max_len + T - 1) / T;
+    if (p.window > 0) {
+        const int64_t span = (int64_t)p.window + (prompt ? (C - 1) / p.G + 1 : 0);
+        const int64_t most = (p.sinks + T - 1) / T + (span + T - 1) / T + 1;
+        nb = nb < most ? nb : most;
+    }
+    nb = nb < 1 ? 1 : nb;
+    const int64_t groups = (int64_t)(prompt ? (a->tokens * (int64_t)p.G + C - 1) / C + a->rows : (int64_t)a->rows * p.tiles) * p.kvh;
+    const int64_t aim = prompt ? kPromptGroups : kDecodeGroups;
+    int64_t splits = groups >= aim ? 1 : aim / groups;
+    if (splits > (nb + kMinBlocks - 1) / kMinBlocks) splits = (nb + kMinBlocks - 1) / kMinBlocks;
+    p.chunk = (int)((nb + splits - 1) / splits);
+    p.splits = (int)((nb + p.chunk - 1) / p.chunk);
+    const int64_t entries = (int64_t)a->tokens * a->q_heads;
+    const int64_t parts = max_parts(entries);
+    if (p.splits > 1 && entries * p.splits > parts) {
+        p.splits = (int)(parts / entries);
+        if (p.splits < 1) p.splits = 1;
+        p.chunk = (int)((nb + p.splits - 1) / p.splits);
+        p.splits = (int)((nb + p.chunk - 1) / p.chunk);
+    }
+    p.part_ml = static_cast<float2*>(a->workspace);
+    p.part_o = reinterpret_cast<float*>(p.part_ml + parts);
+    if ((int64_t)a->rows * p.splits * p.kvh * p.tiles > INT32_MAX) return fail(BCG_ESHAPE, "%s: too many workgroups", who);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (a->q_dtype == BCG_F32) e = prompt ? launch_prompt<float, float>(p, st) : launch_decode<float, float>(p, st);
+    else if (a->kv_dtype == BCG_BF16) e = prompt ? launch_prompt<bf16_t, bf16_t>(p, st) : launch_decode<bf16_t, bf16_t>(p, st);
+    else e = prompt ? launch_prompt<bf16_t, e4m3_t>(p, st) : launch_decode<bf16_t, e4m3_t>(p, st);
+    return hip_status(e, who);
+}
+
+}  // namespace
+
+int prompt_columns(int, int head_dim) { return 64 * (head_dim > 128 ? 1 : 2); }
+
+}  // namespace bcg
+
+extern "C" size_t attention_workspace_size(int tokens, int q_heads, int head_dim) {
+    if (tokens < 1 || q_heads < 1 || head_dim < 1) return 16;
+    return (size_t)bcg::max_parts((int64_t)tokens * q_heads) * (sizeof(float2) + (size_t)head_dim * sizeof(float));
+}
+
+extern "C" int paged_attention(const bcg_attn_args* a, void* stream) { return bcg::run(a, "paged_attention", false, stream); }
+extern "C" int prompt_attention(const bcg_attn_args* a, void* stream) { return bcg::run(a, "prompt_attention", true, stream); }

@@ -1,0 +1,7 @@
+// Paged attention with bf16 queries and e4m3 pages (bcg_attn_impl.h).
+#include "bcg_attn_impl.h"
+
+namespace bcg {
+template hipError_t launch_decode<bf16_t, e4m3_t>(const AttnParams&, hipStream_t);
+template hipError_t launch_prompt<bf16_t, e4m3_t>(const AttnParams&, hipStream_t);
+}  // namespace bcg

@@ -1,0 +1,7 @@
+// Paged attention with fp32 queries and pages (bcg_attn_impl.h).
+#include "bcg_attn_impl.h"
+
+namespace bcg {
+template hipError_t launch_decode<float, float>(const AttnParams&, hipStream_t);
+template hipError_t launch_prompt<float, float>(const AttnParams&, hipStream_t);
+}  // namespace bcg

@@ -1,0 +1,601 @@
+// The paged cache's upkeep: new tokens into the pages, and pages given out,
+// shared, moved and given back.
+//
+// Data moves are plain 16-byte streams (HBM-bound).  The pool's state is the
+// reference counts alone: a page is free when nobody refers to it, and the
+// k-th page asked for is the k-th lowest free one.  So giving back is a
+// decrement (order does not matter), and giving out needs two prefix sums,
+// over the list's needs and over the free pages, which one workgroup computes
+// (a list has as many entries as a batch has rows).
+#include "bcg_device.h"
+#include "bcg_launch.h"
+#include "bcg_decode.h"
+
+namespace bcg {
+namespace {
+
+constexpr int NT = 1024;  // lanes of the bookkeeping workgroup
+
+// ---------------------------------------------------------------- append
+
+struct AppendParams {
+    const void* k;
+    const void* v;
+    const int32_t* off;
+    const int32_t* table;
+    const int32_t* len;
+    const float* kscale;
+    const float* vscale;
+    void* kc;
+    void* vc;
+    int64_t ks, vs, kps, vps;  // elements
+    int rows, tokens, kvh, D, ps, maxb, np, chunks;  // chunks: 8-element chunks of a token
+};
+
+// Eight elements -> the cache's type.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+__device__ __forceinline__ float clamp448(float x) { return x != x ? x : fminf(fmaxf(x, -448.0f), 448.0f); }
+
+// One lane: eight elements of one token's key or value (blockIdx.y).
+template <typename QT, bool E4M3>
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int tok = (int)(id / p.chunks), ch = (int)(id - (int64_t)tok * p.chunks);
+    if (tok >= p.tokens) return;
+    int row = tok, pos;
+    if (p.off) {
+        // the row whose run holds the token: the last one that begins at or before it
+        int a = 0, b = p.rows;  // off[a] <= tok, off[b] > tok
+        if (p.off[0] > tok || p.off[p.rows] <= tok) return;
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (p.off[mid] <= tok) a = mid;
+            else b = mid;
+        }
+        row = a;
+        pos = p.off[row + 1] - tok;
+    } else {
+        pos = 1;
+    }
+    pos = min(max(p.len[row], 0), p.maxb * p.ps) - pos;
+    if (pos < 0) return;
+    const int blk = pos / p.ps, pg = p.table[(int64_t)row * p.maxb + blk];
+    if (pg < 0 || pg >= p.np) return;
+    const int e = ch * 8, h = e / p.D, d = e - h * p.D;
+    const bool val = blockIdx.y != 0;
+    const QT* src = static_cast<const QT*>(val ? p.v : p.k) + (int64_t)tok * (val ? p.vs : p.ks) + e;
+    const int64_t at = (int64_t)pg * (val ? p.vps : p.kps) + ((int64_t)h * p.ps + (pos - blk * p.ps)) * p.D + d;
+    void* dst = val ? p.vc : p.kc;
+    if constexpr (E4M3) {
+        float x[8];
+        Io<QT, 8>::load(src, x);
+        const float s = (val ? p.vscale : p.kscale)[h];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = clamp448(x[i] / s);
+        typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+        u32x2_t w = {e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7])};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)  // one code for NaN: the conversion gives 0xff
+            if (x[i] != x[i]) w[i >> 2] &= ~(0x80u << (i & 3) * 8);
+        *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(dst) + at) = w;
+    } else {
+        constexpr int N = 8 * sizeof(QT) / 16;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            reinterpret_cast<u32x4_t*>(static_cast<QT*>(dst) + at)[i] = reinterpret_cast<const u32x4_t*>(src)[i];
+    }
+}
+
+// ---------------------------------------------------------------- scans
+
+// Sum over the lanes before this one, of one value per lane; `total` gets the
+// workgroup's sum.  Two barriers; ws: NT / 64 words of LDS.
+template <typename I> __device__ __forceinline__ I scan_excl(I x, I* ws, I& total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    I s = x;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+        const I y = __shfl_up(s, k);
+        if (lane >= k) s += y;
+    }
+    __syncthreads();
+    if (lane == 63) ws[wave] = s;
+    __syncthreads();
+    I before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        const I y = ws[w];
+        before += w < wave ? y : I(0);
+        all += y;
+    }
+    total = all;
+    return before + s - x;
+}
+
+// The lowest `want` free pages, ascending, into `fresh`; the count of free
+// pages if it is below `want`, else any number >= want.
+__device__ int find_free(const int32_t* refs, int np, int want, int32_t* fresh, int* ws) {
+    int found = 0;
+    for (int base = 0; base < np && found < want; base += NT * 4) {
+        const int i = base + threadIdx.x * 4;
+        int r[4], n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r[j] = i + j < np ? refs[i + j] : 1;
+            n += r[j] <= 0;
+        }
+        int total;
+        int at = found + scan_excl(n, ws, total);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r[j] <= 0) {
+                if (at < want) fresh[at] = i + j;
+                ++at;
+            }
+        found += total;
+    }
+    __syncthreads();
+    return found;
+}
+
+struct CacheParams {
+    int planes, np, ps, rows, maxb;
+    int64_t plane, page;  // bytes between planes, pages
+    int vecs;             // 16-byte vectors of a page
+    uint8_t* pool;
+    int32_t* table;
+    int32_t* len;
+    int32_t* refs;
+    // workspace
+    int32_t* owner;  // [rows] first list entry that names the row
+    int32_t* need;   // [n] pages needed by the entry, -1: refused
+    int32_t* fresh;  // [num_pages] the free pages found
+    int32_t* pair;   // [2n or 2 num_pages] pages to copy: from, to
+};
+
+// owner[row] = the first entry of the list that names it.
+__device__ void first_entries(const CacheParams& p, int n, const int32_t* list) {
+    for (int i = threadIdx.x; i < n; i += NT)
+        if (list[i] >= 0 && list[i] < p.rows) p.owner[list[i]] = n;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += NT)
+        if (list[i] >= 0 && list[i] < p.rows) atomicMin(&p.owner[list[i]], i);
+    __syncthreads();
+}
+
+__device__ __forceinline__ int row_len(const CacheParams& p, int row) { return min(max(p.len[row], 0), p.maxb * p.ps); }
+
+// ---------------------------------------------------------------- extend, fork
+
+__global__ void __launch_bounds__(NT) extend_kernel(const CacheParams p, int n, const int32_t* rows, const int32_t* count, int32_t* granted) {
+    __shared__ int ws[NT / 64];
+    __shared__ int64_t ws64[NT / 64];  // a list's needs can pass 32 bits
+    first_entries(p, n, rows);
+    int64_t want = 0;
+    for (int base = 0; base < n; base += NT) {
+        const int i = base + threadIdx.x;
+        int need = 0, ok = 0;
+        if (i < n && rows[i] >= 0 && rows[i] < p.rows && p.owner[rows[i]] == i && count[i] >= 0) {
+            const int len = row_len(p, rows[i]);
+            const int64_t to = (int64_t)len + count[i];
+            if (to <= (int64_t)p.maxb * p.ps) {
+                ok = 1;
+                need = (int)((to + p.ps - 1) / p.ps) - (len + p.ps - 1) / p.ps;
+            }
+        }
+        int64_t total;
+        scan_excl<int64_t>(need, ws64, total);
+        if (i < n) p.need[i] = ok ? need : -1;
+        want += total;
+    }
+    const int found = find_free(p.refs, p.np, (int)min(want, (int64_t)p.np), p.fresh, ws);
+    int64_t before = 0;
+    for (int base = 0; base < n; base += NT) {
+        const int i = base + threadIdx.x;
+        const int need = i < n ? p.need[i] : -1;
+        int64_t total;
+        const int64_t at = before + scan_excl<int64_t>(max(need, 0), ws64, total);
+        before += total;
+        if (i < n) {
+            const bool ok = need >= 0 && (need == 0 || at + need <= found);
+            granted[i] = ok;
+            if (ok) {
+                const int row = rows[i], len = row_len(p, row), b = (len + p.ps - 1) / p.ps;
+                for (int k = 0; k < need; ++k) {
+                    const int pg = p.fresh[at + k];
+                    p.table[(int64_t)row * p.maxb + b + k] = pg;
+                    p.refs[pg] = 1;
+                }
+                p.len[row] = len + count[i];
+            }
+        }
+    }
+}
+
+// Which forks go ahead, and the page of each one's partly filled last block.
+// Leaves pair[2i] = page to copy or -1, pair[2i + 1] = where to, need[i] = -1
+// where refused, else the length.
+__global__ void __launch_bounds__(NT) fork_kernel(const CacheParams p, int n, const int32_t* src, const int32_t* dst, int32_t* granted) {
+    __shared__ int ws[NT / 64];
+    first_entries(p, n, dst);
+    int want = 0;
+    for (int base = 0; base < n; base += NT) {
+        const int i = base + threadIdx.x;
+        int len = -1, part = -1;
+        if (i < n) {
+            const int s = src[i], d = dst[i];
+            if (s >= 0 && s < p.rows && d >= 0 && d < p.rows && s != d && p.owner[d] == i && p.len[d] == 0 &&
+                (p.maxb == 0 || p.table[(int64_t)d * p.maxb] < 0)) {
+                len = row_len(p, s);
+                if (len % p.ps) part = p.table[(int64_t)s * p.maxb + len / p.ps];
+                if (part >= p.np) part = -1;
+            }
+            p.need[i] = len;
+            p.pair[2 * i] = part;
+        }
+        int total;
+        scan_excl(part >= 0 ? 1 : 0, ws, total);
+        want += total;
+    }
+    const int found = find_free(p.refs, p.np, min(want, p.np), p.fresh, ws);
+    int before = 0;
+    for (int base = 0; base < n; base += NT) {
+        const int i = base + threadIdx.x;
+        const int len = i < n ? p.need[i] : -1, part = i < n ? p.pair[2 * i] : -1;
+        int total;
+        const int at = before + scan_excl(part >= 0 ? 1 : 0, ws, total);
+        before += total;
+        if (i < n) {
+            const bool ok = len >= 0 && (part < 0 || at < found);
+            granted[i] = ok;
+            if (!ok) {
+                p.need[i] = -1;
+                p.pair[2 * i] = -1;
+            } else if (part >= 0) {
+                p.pair[2 * i + 1] = p.fresh[at];
+                p.refs[p.fresh[at]] = 1;
+            }
+        }
+    }
+}
+
+// After fork_kernel: blocks [0, n) copy fork i's table row; the others copy
+// the partly filled pages, one (fork, plane, part) at a time.
+__device__ __forceinline__ void copy_page(const CacheParams& p, int plane, int from, int to, int v0, int v1) {
+    const u32x4_t* a = reinterpret_cast<const u32x4_t*>(p.pool + plane * p.plane + from * p.page);
+    u32x4_t* b = reinterpret_cast<u32x4_t*>(p.pool + plane * p.plane + to * p.page);
+    int v = v0 + threadIdx.x;
+    for (; v + 3 * 256 < v1; v += 4 * 256) {
+        u32x4_t x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = a[v + j * 256];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[v + j * 256] = x[j];
+    }
+    for (; v < v1; v += 256) b[v] = a[v];
+}
+
+constexpr int kPart = 2048;  // vectors (32 KB) of a page that one workgroup copies at a time
+
+__global__ void __launch_bounds__(256) fork_copy_kernel(const CacheParams p, int n, const int32_t* src, const int32_t* dst) {
+    if ((int)blockIdx.x < n) {
+        const int i = blockIdx.x, len = p.need[i];
+        if (len < 0) return;
+        const int32_t* a = p.table + (int64_t)src[i] * p.maxb;
+        int32_t* b = p.table + (int64_t)dst[i] * p.maxb;
+        const int full = len / p.ps;
+        for (int k = threadIdx.x; k < p.maxb; k += 256) {
+            int pg = -1;
+            if (k < full) {
+                pg = a[k];
+                if (pg >= 0 && pg < p.np) atomicAdd(&p.refs[pg], 1);
+                else pg = -1;
+            } else if (k == full && p.pair[2 * i] >= 0) {
+                pg = p.pair[2 * i + 1];
+            }
+            b[k] = pg;
+        }
+        if (threadIdx.x == 0) p.len[dst[i]] = len;
+        return;
+    }
+    const int parts = (p.vecs + kPart - 1) / kPart;
+    const int64_t items = (int64_t)n * p.planes * parts;
+    for (int64_t it = blockIdx.x - n; it < items; it += gridDim.x - n) {
+        const int part = (int)(it % parts), plane = (int)(it / parts % p.planes), i = (int)(it / parts / p.planes);
+        if (p.pair[2 * i] < 0) continue;
+        copy_page(p, plane, p.pair[2 * i], p.pair[2 * i + 1], part * kPart, min(p.vecs, part * kPart + kPart));
+    }
+}
+
+// ---------------------------------------------------------------- free
+
+// Block (list entry, range of table columns).  An entry that several list
+// entries name is given back once: it is taken out of the table atomically.
+__global__ void __launch_bounds__(256) free_kernel(const CacheParams p, const int32_t* rows, int window, int sinks) {
+    const int row = rows[blockIdx.y];
+    if (row < 0 || row >= p.rows) return;
+    const int b = blockIdx.x * 256 + threadIdx.x;
+    if (b >= p.maxb) return;
+    if (window > 0) {
+        const int len = row_len(p, row), lo = len - window + 1;  // the tokens from lo on stay
+        const int64_t t0 = (int64_t)b * p.ps;
+        if (t0 < sinks || t0 + p.ps > lo || t0 + p.ps > len) return;
+    }
+    int32_t* e = p.table + (int64_t)row * p.maxb + b;
+    if (*e < 0) return;
+    const int pg = atomicExch(e, -1);
+    if (pg >= 0 && pg < p.np) atomicSub(&p.refs[pg], 1);
+}
+__global__ void __launch_bounds__(256) clear_len_kernel(const CacheParams p, int n, const int32_t* rows) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i < n && rows[i] >= 0 && rows[i] < p.rows) p.len[rows[i]] = 0;
+}
+
+// ---------------------------------------------------------------- compact
+
+// The moves: fresh[p] = new place of page p; pair[2k], pair[2k + 1] = from, to
+// of move k; owner[0] = their count (rows >= 1) -- kept in pair's last word.
+__global__ void __launch_bounds__(NT) compact_plan_kernel(const CacheParams p, int32_t* refs_out, int32_t* moved) {
+    __shared__ int ws[NT / 64];
+    int live = 0;
+    for (int base = 0; base < p.np; base += NT * 4) {
+        const int i = base + threadIdx.x * 4;
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n += i + j < p.np && p.refs[i + j] > 0;
+        int total;
+        scan_excl(n, ws, total);
+        live += total;
+    }
+    int holes = 0, movers = 0;
+    for (int base = 0; base < p.np; base += NT * 4) {
+        const int i = base + threadIdx.x * 4;
+        int r[4], nh = 0, nm = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r[j] = i + j < p.np ? p.refs[i + j] : 0;
+            nh += i + j < live && r[j] <= 0;
+            nm += i + j >= live && r[j] > 0;
+        }
+        int th, tm;
+        int ah = holes + scan_excl(nh, ws, th), am = movers + scan_excl(nm, ws, tm);
+        holes += th;
+        movers += tm;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (i + j >= p.np) continue;
+            p.fresh[i + j] = i + j;
+            if (i + j < live && r[j] <= 0) p.pair[2 * ah++ + 1] = i + j;
+            if (i + j >= live && r[j] > 0) p.pair[2 * am++] = i + j;
+        }
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < movers; k += NT) p.fresh[p.pair[2 * k]] = p.pair[2 * k + 1];
+    __syncthreads();
+    // the counts move along; in place this is safe: a hole's count is not read again
+    for (int i = threadIdx.x; i < p.np; i += NT) {
+        const int r = p.refs[i];
+        if (i < live && r > 0) refs_out[i] = r;
+    }
+    for (int k = threadIdx.x; k < movers; k += NT) refs_out[p.pair[2 * k + 1]] = p.refs[p.pair[2 * k]];
+    __syncthreads();
+    for (int i = live + threadIdx.x; i < p.np; i += NT) refs_out[i] = 0;
+    if (threadIdx.x == 0) {
+        p.owner[0] = movers;
+        if (moved) *moved = movers;
+    }
+}
+
+__global__ void __launch_bounds__(256) compact_copy_kernel(const CacheParams p, int tblocks, int32_t* table_out) {
+    if ((int)blockIdx.x < tblocks) {
+        const int64_t n = (int64_t)p.rows * p.maxb;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)tblocks * 256) {
+            const int pg = p.table[i];
+            table_out[i] = pg >= 0 && pg < p.np ? p.fresh[pg] : -1;
+        }
+        return;
+    }
+    const int parts = (p.vecs + kPart - 1) / kPart, n = p.owner[0];
+    const int64_t items = (int64_t)n * p.planes * parts;
+    for (int64_t it = blockIdx.x - tblocks; it < items; it += gridDim.x - tblocks) {
+        const int part = (int)(it % parts), plane = (int)(it / parts % p.planes), k = (int)(it / parts / p.planes);
+        copy_page(p, plane, p.pair[2 * k], p.pair[2 * k + 1], part * kPart, min(p.vecs, part * kPart + kPart));
+    }
+}
+
+// ---------------------------------------------------------------- copy
+
+__global__ void __launch_bounds__(256) copy_kernel(const CacheParams p, int n, const int32_t* src, const int32_t* dst) {
+    const int parts = (p.vecs + kPart - 1) / kPart;
+    const int64_t items = (int64_t)n * p.planes * parts;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int part = (int)(it % parts), plane = (int)(it / parts % p.planes), i = (int)(it / parts / p.planes);
+        const int a = src[i], b = dst[i];
+        if (a < 0 || a >= p.np || b < 0 || b >= p.np) continue;
+        copy_page(p, plane, a, b, part * kPart, min(p.vecs, part * kPart + kPart));
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr int64_t kCopyGroups = 256 * 8;  // one resident round of copying workgroups
+
+size_t words16(int64_t n) { return (size_t)((n + 3) / 4 * 4); }
+
+unsigned copy_groups(const CacheParams& p, int64_t n) {
+    const int64_t items = n * p.planes * ((p.vecs + kPart - 1) / kPart);
+    return (unsigned)(items < 1 ? 1 : (items < kCopyGroups ? items : kCopyGroups));
+}
+
+// What every pool operator checks; fills the launch parameters.
+int setup(const bcg_cache* c, const char* who, int n, bool tables, CacheParams& p) {
+    if (!c) return fail(BCG_EINVAL, "%s: cache is NULL", who);
+    if (c->planes < 1 || c->planes > (1 << 16) || c->num_pages < 1 || c->num_pages > (1 << 28))
+        return fail(BCG_ESHAPE, "%s: %d planes of %d pages", who, c->planes, c->num_pages);
+    if (n < 0 || n > (1 << 24)) return fail(BCG_ESHAPE, "%s: a list of %d entries", who, n);
+    if (!c->pool) return fail(BCG_EINVAL, "%s: NULL pool", who);
+    if (c->page_bytes < 16 || c->page_bytes > (1ll << 30) || c->page_bytes > c->page_stride || c->plane_stride < 0)
+        return fail(BCG_EINVAL, "%s: pages of %lld bytes, %lld apart", who, (long long)c->page_bytes, (long long)c->page_stride);
+    if (!aligned16(c->pool) || c->page_bytes % 16 || c->page_stride % 16 || c->plane_stride % 16)
+        return fail(BCG_EINVAL, "%s: the pool, its planes and pages must be 16-byte aligned", who);
+    p.planes = c->planes; p.np = c->num_pages; p.plane = c->plane_stride; p.page = c->page_stride;
+    p.vecs = (int)(c->page_bytes / 16);
+    p.pool = static_cast<uint8_t*>(c->pool);
+    if (!tables) return BCG_OK;
+    if (c->page_size < 1 || c->page_size > BCG_MAX_PAGE_SIZE || c->rows < 1 || c->max_blocks < 0 ||
+        (int64_t)c->max_blocks * c->page_size > (1 << 30))
+        return fail(BCG_ESHAPE, "%s: %d rows of %d blocks of %d tokens", who, c->rows, c->max_blocks, c->page_size);
+    if ((c->max_blocks > 0 && !c->block_table) || !c->kv_len || !c->refs) return fail(BCG_EINVAL, "%s: NULL table", who);
+    const size_t need = cache_workspace_size(c->rows, c->num_pages, n);
+    if (!c->workspace || !aligned16(c->workspace) || c->workspace_bytes < need)
+        return fail(BCG_EINVAL, "%s: a workspace of %zu bytes is needed, 16-byte aligned (%zu given)", who, need, c->workspace_bytes);
+    p.ps = c->page_size; p.rows = c->rows; p.maxb = c->max_blocks;
+    p.table = c->block_table; p.len = c->kv_len; p.refs = c->refs;
+    p.owner = static_cast<int32_t*>(c->workspace);
+    p.need = p.owner + words16(c->rows);
+    p.fresh = p.need + words16(n);
+    p.pair = p.fresh + words16(c->num_pages);
+    return BCG_OK;
+}
+
+}  // namespace
+}  // namespace bcg
+
+using namespace bcg;
+
+extern "C" size_t cache_workspace_size(int rows, int num_pages, int n) {
+    if (rows < 1 || num_pages < 1 || n < 0) return 16;
+    const int64_t pairs = n > num_pages ? n : num_pages;
+    return (words16(rows) + words16(n) + words16(num_pages) + words16(2 * pairs)) * sizeof(int32_t);
+}
+
+extern "C" int cache_append(const bcg_append_args* a, void* stream) {
+    clear_error();
+    const char* who = "cache_append";
+    if (!a) return fail(BCG_EINVAL, "%s: args is NULL", who);
+    if (a->rows < 0 || a->tokens < 0 || a->tokens > (1 << 24)) return fail(BCG_ESHAPE, "%s: rows %d, tokens %d", who, a->rows, a->tokens);
+    if (!a->offset && a->rows != a->tokens) return fail(BCG_ESHAPE, "%s: %d rows but %d tokens", who, a->rows, a->tokens);
+    if (a->kv_heads < 1 || a->kv_heads > 4096) return fail(BCG_ESHAPE, "%s: %d kv heads", who, a->kv_heads);
+    if ((a->dtype != BCG_F32 && a->dtype != BCG_BF16) || (a->kv_dtype != a->dtype && !(a->kv_dtype == BCG_E4M3 && a->dtype == BCG_BF16)))
+        return fail(BCG_EDTYPE, "%s: tokens of type %d into a cache of type %d", who, a->dtype, a->kv_dtype);
+    const int unit = a->kv_dtype == BCG_E4M3 ? 16 : 8;
+    if (a->head_dim < unit || a->head_dim > BCG_MAX_HEAD_DIM || a->head_dim % unit != 0)
+        return fail(BCG_ESHAPE, "%s: head_dim %d is not a multiple of %d up to %d", who, a->head_dim, unit, BCG_MAX_HEAD_DIM);
+    if (a->page_size < 16 || a->page_size > BCG_MAX_PAGE_SIZE || a->page_size % 16 != 0)
+        return fail(BCG_ESHAPE, "%s: page_size %d is not a multiple of 16 up to %d", who, a->page_size, BCG_MAX_PAGE_SIZE);
+    if (a->max_blocks < 0 || (int64_t)a->max_blocks * a->page_size > (1 << 30) || a->num_pages < 0)
+        return fail(BCG_ESHAPE, "%s: %d blocks of %d tokens, %d pages", who, a->max_blocks, a->page_size, a->num_pages);
+    if (a->rows == 0 || a->tokens == 0 || a->max_blocks == 0 || a->num_pages == 0) return BCG_OK;
+    if (!a->k || !a->v || !a->block_table || !a->kv_len || !a->k_cache || !a->v_cache) return fail(BCG_EINVAL, "%s: NULL device pointer", who);
+    if (a->kv_dtype == BCG_E4M3 && (!a->k_scale || !a->v_scale)) return fail(BCG_EINVAL, "%s: an e4m3 cache needs its scales", who);
+    if (a->kv_dtype != BCG_E4M3 && (a->k_scale || a->v_scale)) return fail(BCG_EINVAL, "%s: scales are those of an e4m3 cache", who);
+    const int64_t es = (int64_t)elem_size(a->dtype), cs = a->kv_dtype == BCG_E4M3 ? 1 : es, width = (int64_t)a->kv_heads * a->head_dim;
+    if (a->k_stride < width || a->v_stride < width) return fail(BCG_ESHAPE, "%s: token strides %lld, %lld", who, (long long)a->k_stride, (long long)a->v_stride);
+    if (a->k_page_stride < width * a->page_size || a->v_page_stride < width * a->page_size)
+        return fail(BCG_ESHAPE, "%s: page strides %lld, %lld below a page's %lld", who, (long long)a->k_page_stride,
+                    (long long)a->v_page_stride, (long long)(width * a->page_size));
+    if (!aligned16(a->k) || !aligned16(a->v) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || a->k_stride * es % 16 ||
+        a->v_stride * es % 16 || a->k_page_stride * cs % 16 || a->v_page_stride * cs % 16)
+        return fail(BCG_EINVAL, "%s: tokens, caches and pages must be 16-byte aligned", who);
+    AppendParams p{};
+    p.k = a->k; p.v = a->v; p.off = a->offset; p.table = a->block_table; p.len = a->kv_len;
+    p.kscale = a->k_scale; p.vscale = a->v_scale; p.kc = a->k_cache; p.vc = a->v_cache;
+    p.ks = a->k_stride; p.vs = a->v_stride; p.kps = a->k_page_stride; p.vps = a->v_page_stride;
+    p.rows = a->rows; p.tokens = a->tokens; p.kvh = a->kv_heads; p.D = a->head_dim;
+    p.ps = a->page_size; p.maxb = a->max_blocks; p.np = a->num_pages; p.chunks = (int)(width / 8);
+    const int64_t blocks = ((int64_t)a->tokens * p.chunks + 255) / 256;
+    if (blocks > INT32_MAX) return fail(BCG_ESHAPE, "%s: too many tokens", who);
+    const dim3 grid((unsigned)blocks, 2);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (a->kv_dtype == BCG_E4M3) hipLaunchKernelGGL((append_kernel<bf16_t, true>), grid, dim3(256), 0, st, p);
+    else if (a->dtype == BCG_BF16) hipLaunchKernelGGL((append_kernel<bf16_t, false>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((append_kernel<float, false>), grid, dim3(256), 0, st, p);
+    return hip_status(hipGetLastError(), "cache_append: launch");
+}
+
+extern "C" int cache_extend(const bcg_cache* c, int n, const int32_t* rows, const int32_t* count, int32_t* granted, void* stream) {
+    clear_error();
+    CacheParams p{};
+    const int rc = setup(c, "cache_extend", n, true, p);
+    if (rc != BCG_OK) return rc;
+    if (n == 0) return BCG_OK;
+    if (!rows || !count || !granted) return fail(BCG_EINVAL, "cache_extend: NULL list");
+    hipLaunchKernelGGL(extend_kernel, dim3(1), dim3(NT), 0, static_cast<hipStream_t>(stream), p, n, rows, count, granted);
+    return hip_status(hipGetLastError(), "cache_extend: launch");
+}
+
+extern "C" int cache_fork(const bcg_cache* c, int n, const int32_t* src, const int32_t* dst, int32_t* granted, void* stream) {
+    clear_error();
+    CacheParams p{};
+    const int rc = setup(c, "cache_fork", n, true, p);
+    if (rc != BCG_OK) return rc;
+    if (n == 0) return BCG_OK;
+    if (!src || !dst || !granted) return fail(BCG_EINVAL, "cache_fork: NULL list");
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipLaunchKernelGGL(fork_kernel, dim3(1), dim3(NT), 0, st, p, n, src, dst, granted);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess) {
+        hipLaunchKernelGGL(fork_copy_kernel, dim3(n + copy_groups(p, n)), dim3(256), 0, st, p, n, src, dst);
+        e = hipGetLastError();
+    }
+    return hip_status(e, "cache_fork: launch");
+}
+
+extern "C" int cache_free(const bcg_cache* c, int n, const int32_t* rows, int window, int sinks, void* stream) {
+    clear_error();
+    CacheParams p{};
+    const int rc = setup(c, "cache_free", n, true, p);
+    if (rc != BCG_OK) return rc;
+    if (window < 0 || sinks < 0) return fail(BCG_EINVAL, "cache_free: window %d, sinks %d", window, sinks);
+    if (n == 0) return BCG_OK;
+    if (n > 65535) return fail(BCG_ESHAPE, "cache_free: a list of %d entries (at most 65535)", n);
+    if (!rows) return fail(BCG_EINVAL, "cache_free: NULL list");
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (p.maxb > 0) {
+        hipLaunchKernelGGL(free_kernel, dim3((unsigned)((p.maxb + 255) / 256), n), dim3(256), 0, st, p, rows, window, sinks);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && window == 0) {
+        hipLaunchKernelGGL(clear_len_kernel, dim3((n + 255) / 256), dim3(256), 0, st, p, n, rows);
+        e = hipGetLastError();
+    }
+    return hip_status(e, "cache_free: launch");
+}
+
+extern "C" int cache_compact(const bcg_cache* c, int32_t* table_out, int32_t* refs_out, int32_t* moved, void* stream) {
+    clear_error();
+    const char* who = "cache_compact";
+    CacheParams p{};
+    const int rc = setup(c, who, 0, true, p);
+    if (rc != BCG_OK) return rc;
+    if (!refs_out || (p.maxb > 0 && !table_out)) return fail(BCG_EINVAL, "%s: NULL output", who);
+    const size_t tb = (size_t)p.rows * p.maxb * 4, rb = (size_t)p.np * 4;
+    if (partial_overlap(p.table, table_out, tb) || partial_overlap(p.refs, refs_out, rb) || any_overlap(p.table, tb, refs_out, rb) ||
+        any_overlap(p.refs, rb, table_out, tb))
+        return fail(BCG_EINVAL, "%s: outputs overlap the tables in part", who);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipLaunchKernelGGL(compact_plan_kernel, dim3(1), dim3(NT), 0, st, p, refs_out, moved);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess) {
+        const int64_t t = ((int64_t)p.rows * p.maxb + 255) / 256;
+        const int tblocks = (int)(t < 256 ? t : 256);
+        hipLaunchKernelGGL(compact_copy_kernel, dim3(tblocks + copy_groups(p, p.np)), dim3(256), 0, st, p, tblocks, table_out);
+        e = hipGetLastError();
+    }
+    return hip_status(e, "cache_compact: launch");
+}
+
+extern "C" int cache_copy(const bcg_cache* c, int n, const int32_t* src, const int32_t* dst, void* stream) {
+    clear_error();
+    CacheParams p{};
+    const int rc = setup(c, "cache_copy", n, false, p);
+    if (rc != BCG_OK) return rc;
+    if (n == 0) return BCG_OK;
+    if (!src || !dst) return fail(BCG_EINVAL, "cache_copy: NULL list");
+    hipLaunchKernelGGL(copy_kernel, dim3(copy_groups(p, n)), dim3(256), 0, static_cast<hipStream_t>(stream), p, n, src, dst);
+    return hip_status(hipGetLastError(), "cache_copy: launch");
+}

@@ -1,0 +1,215 @@
+// guided_logits: the guided combine of two branches' logits with penalties,
+// biases, temperature and a grammar mask, in one pass over the vocabulary.
+//
+// HBM-bound: per token it reads c and u, writes z, and does a few fp32
+// operations.  A workgroup takes kSeg consecutive tokens of one sample.  The
+// sparse inputs (the history's tokens, the biased ids) become dense in LDS
+// first: the workgroup runs over the sample's lists and counts those that
+// fall into its tokens, while its logits are on their way.  Integer counts
+// and the largest index win by LDS atomics, so no order changes a result.
+#include "bcg_device.h"
+#include "bcg_launch.h"
+#include "bcg_decode.h"
+
+namespace bcg {
+namespace {
+
+constexpr int NT = 256;
+constexpr int kVec = 8;                 // tokens of one lane's vector
+constexpr int kRounds = 2;              // vectors of a lane
+constexpr int kSeg = NT * kVec * kRounds;
+
+struct LogitsParams {
+    int n, vocab, rows, hist, biases, words;
+    int64_t stride, out_stride;
+    const void* logits;
+    void* out;
+    const int32_t* cond;
+    const int32_t* uncond;
+    const float* scale;
+    const int32_t* history;
+    const int32_t* hlen;
+    const int32_t* plen;
+    const float* rep;
+    const float* pres;
+    const float* freq;
+    const int32_t* bias_ids;
+    const float* bias;
+    const float* temp;
+    const uint8_t* mask;
+};
+
+// Eight elements at an address aligned to one: odd vocabularies and strides
+// put rows anywhere, and gfx950 takes 16-byte accesses at any address.
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16_t> {
+    struct __attribute__((packed, aligned(2))) V { u32x4_t x; } v;
+    __device__ __forceinline__ void get(float (&o)[8]) const { Io<bf16_t, 8>::unpack(v.x, o); }
+    __device__ __forceinline__ void set(const float (&o)[8]) { v.x = Io<bf16_t, 8>::pack(o); }
+};
+template <> struct Raw8<float> {
+    struct __attribute__((packed, aligned(4))) V { f32x4_t x, y; } v;
+    __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { o[i] = v.x[i]; o[4 + i] = v.y[i]; }
+    }
+    __device__ __forceinline__ void set(const float (&o)[8]) {
+        v.x = f32x4_t{o[0], o[1], o[2], o[3]};
+        v.y = f32x4_t{o[4], o[5], o[6], o[7]};
+    }
+};
+template <typename T> __device__ __forceinline__ void load8(const T* p, int left, float (&o)[8]) {
+    if (left >= 8) {
+        Raw8<T> r;
+        r.v = *reinterpret_cast<const typename Raw8<T>::V*>(p);
+        r.get(o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float x[1] = {0.0f};
+            if (i < left) Io<T, 1>::load(p + i, x);
+            o[i] = x[0];
+        }
+    }
+}
+template <typename T> __device__ __forceinline__ void store8(T* p, int left, const float (&o)[8]) {
+    if (left >= 8) {
+        Raw8<T> r;
+        r.set(o);
+        *reinterpret_cast<typename Raw8<T>::V*>(p) = r.v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) Io<T, 1>::store(p + i, {o[i]});
+    }
+}
+
+template <typename T, typename OT, bool SPARSE>
+__global__ void __launch_bounds__(NT) logits_kernel(const LogitsParams p) {
+    __shared__ uint32_t cnt[SPARSE ? kSeg : 1];   // 0: not in the history; low 31 bits: times in the answer
+    __shared__ uint32_t last[SPARSE ? kSeg : 1];  // 1 + the last bias of the token, 0: none
+    const int i = blockIdx.y, s0 = blockIdx.x * kSeg, tid = threadIdx.x;
+    const int cr = p.cond[i];
+    if (cr < 0 || cr >= p.rows) return;
+    const float w = p.scale ? p.scale[i] : 1.0f;
+    int ur = p.uncond ? p.uncond[i] : -1;
+    if (ur >= p.rows) ur = -1;
+    const bool guided = ur >= 0 && w != 1.0f;
+    const T* crow = static_cast<const T*>(p.logits) + (int64_t)cr * p.stride;
+    const T* urow = static_cast<const T*>(p.logits) + (int64_t)(guided ? ur : cr) * p.stride;
+
+    float c[kRounds][8], u[kRounds][8];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int j = s0 + (r * NT + tid) * kVec;
+        load8<T>(crow + j, p.vocab - j, c[r]);
+        if (guided) load8<T>(urow + j, p.vocab - j, u[r]);
+    }
+    if constexpr (SPARSE) {
+        for (int k = tid; k < kSeg; k += NT) cnt[k] = last[k] = 0u;
+        __syncthreads();
+        if (p.history) {
+            const int hl = min(max(p.hlen[i], 0), p.hist), pl = p.plen ? p.plen[i] : 0;
+            const int32_t* h = p.history + (int64_t)i * p.hist;
+            for (int k = tid; k < hl; k += NT) {
+                const unsigned at = (unsigned)(h[k] - s0);
+                if (at < (unsigned)kSeg) {
+                    if (k >= pl) atomicAdd(&cnt[at], 1u);
+                    else atomicOr(&cnt[at], 0x80000000u);
+                }
+            }
+        }
+        if (p.bias_ids) {
+            const int32_t* b = p.bias_ids + (int64_t)i * p.biases;
+            for (int k = tid; k < p.biases; k += NT) {
+                const unsigned at = (unsigned)(b[k] - s0);
+                if (at < (unsigned)kSeg) atomicMax(&last[at], (unsigned)k + 1u);
+            }
+        }
+        __syncthreads();
+    }
+    const float rep = p.rep ? p.rep[i] : 1.0f, pres = p.pres ? p.pres[i] : 0.0f, freq = p.freq ? p.freq[i] : 0.0f;
+    const float temp = p.temp ? p.temp[i] : 1.0f;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int j = s0 + (r * NT + tid) * kVec, left = p.vocab - j;
+        if (left <= 0) break;
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = guided && u[r][e] != c[r][e] ? __builtin_fmaf(w, c[r][e] - u[r][e], u[r][e]) : c[r][e];
+        if constexpr (SPARSE) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t n = cnt[j - s0 + e], b = last[j - s0 + e];
+                if (n) {
+                    z[e] = z[e] > 0.0f ? z[e] / rep : z[e] * rep;
+                    const uint32_t m = n & 0x7fffffffu;
+                    z[e] = z[e] - freq * (float)m;
+                    if (m) z[e] = z[e] - pres;
+                }
+                if (b) z[e] = z[e] + p.bias[(int64_t)i * p.biases + b - 1];
+            }
+        }
+        if (temp != 1.0f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = z[e] / temp;
+        }
+        if (p.mask) {
+            const uint32_t bits = p.mask[(int64_t)i * p.words * 4 + (j >> 3)];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = bits >> e & 1u ? z[e] : -__builtin_inff();
+        }
+        store8<OT>(static_cast<OT*>(p.out) + (int64_t)i * p.out_stride + j, left, z);
+    }
+}
+
+template <typename T, typename OT> hipError_t launch(const LogitsParams& p, hipStream_t st) {
+    const dim3 grid((unsigned)((p.vocab + kSeg - 1) / kSeg), (unsigned)p.n);
+    if (p.history || p.bias_ids) hipLaunchKernelGGL((logits_kernel<T, OT, true>), grid, dim3(NT), 0, st, p);
+    else hipLaunchKernelGGL((logits_kernel<T, OT, false>), grid, dim3(NT), 0, st, p);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace bcg
+
+using namespace bcg;
+
+extern "C" int guided_logits(const bcg_logits_args* a, void* stream) {
+    clear_error();
+    const char* who = "guided_logits";
+    if (!a) return fail(BCG_EINVAL, "%s: args is NULL", who);
+    if (a->n < 0 || a->n > 65535 || a->vocab < 0 || a->vocab > (1 << 30) || a->logit_rows < 0)
+        return fail(BCG_ESHAPE, "%s: n %d (at most 65535), vocab %d, %d rows", who, a->n, a->vocab, a->logit_rows);
+    if ((a->dtype != BCG_F32 && a->dtype != BCG_BF16) || (a->out_dtype != BCG_F32 && a->out_dtype != BCG_BF16))
+        return fail(BCG_EDTYPE, "%s: unknown dtype (logits %d, out %d)", who, a->dtype, a->out_dtype);
+    if (a->n == 0 || a->vocab == 0 || a->logit_rows == 0) return BCG_OK;
+    if (!a->logits || !a->out || !a->cond_row) return fail(BCG_EINVAL, "%s: NULL device pointer", who);
+    if (a->uncond_row && !a->scale) return fail(BCG_EINVAL, "%s: uncond rows without a scale", who);
+    if (a->logit_stride < a->vocab || a->out_stride < a->vocab)
+        return fail(BCG_ESHAPE, "%s: row strides %lld, %lld below the vocabulary's %d", who, (long long)a->logit_stride,
+                    (long long)a->out_stride, a->vocab);
+    const bool penal = a->repetition || a->presence || a->frequency || a->prompt_len || a->history_len;
+    if (!a->history && penal) return fail(BCG_EINVAL, "%s: penalties without a history", who);
+    if (a->history && (!a->history_len || a->max_history < 0)) return fail(BCG_EINVAL, "%s: a history without its lengths", who);
+    if ((a->bias_ids == nullptr) != (a->bias == nullptr)) return fail(BCG_EINVAL, "%s: bias and bias_ids go together", who);
+    if (a->bias_ids && (a->num_biases < 0 || a->num_biases > BCG_MAX_BIASES))
+        return fail(BCG_ESHAPE, "%s: %d biases not in [0, %d]", who, a->num_biases, BCG_MAX_BIASES);
+    if (a->mask && a->mask_words < (a->vocab + 31) / 32) return fail(BCG_ESHAPE, "%s: %d mask words for %d tokens", who, a->mask_words, a->vocab);
+    const size_t lb = ((size_t)(a->logit_rows - 1) * a->logit_stride + a->vocab) * elem_size(a->dtype);
+    const size_t ob = ((size_t)(a->n - 1) * a->out_stride + a->vocab) * elem_size(a->out_dtype);
+    if (any_overlap(a->logits, lb, a->out, ob)) return fail(BCG_EINVAL, "%s: out overlaps logits", who);
+    LogitsParams p{};
+    p.n = a->n; p.vocab = a->vocab; p.rows = a->logit_rows; p.hist = a->max_history; p.biases = a->num_biases; p.words = a->mask_words;
+    p.stride = a->logit_stride; p.out_stride = a->out_stride; p.logits = a->logits; p.out = a->out;
+    p.cond = a->cond_row; p.uncond = a->uncond_row; p.scale = a->scale;
+    p.history = a->max_history > 0 ? a->history : nullptr; p.hlen = a->history_len; p.plen = a->prompt_len;
+    p.rep = a->repetition; p.pres = a->presence; p.freq = a->frequency;
+    p.bias_ids = a->num_biases > 0 ? a->bias_ids : nullptr; p.bias = a->bias; p.temp = a->temperature;
+    p.mask = reinterpret_cast<const uint8_t*>(a->mask);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (a->dtype == BCG_BF16) e = a->out_dtype == BCG_BF16 ? launch<bf16_t, bf16_t>(p, st) : launch<bf16_t, float>(p, st);
+    else e = a->out_dtype == BCG_BF16 ? launch<float, bf16_t>(p, st) : launch<float, float>(p, st);
+    return hip_status(e, "guided_logits: launch");
+}

@@ -1,0 +1,257 @@
+/*
+ * bcg_decode.h -- C ABI of libbcg, second part: guided decoding of token
+ * models on AMD Instinct MI355X (gfx950).  A model whose answers are tokens
+ * takes the same bucketed guidance as a denoiser: the plan of bcg.h gives
+ * every sample its scale and its rows of the [uncond | cond] batch.  The
+ * operators here are what such a step needs next to it: attention over a
+ * paged key-value cache, the cache's upkeep, and the guided logits.
+ *
+ * Conventions are those of bcg.h: int status codes and bcg_last_error(),
+ * arguments validated before anything is launched, no allocation and no
+ * synchronisation, device work on the caller's stream.  Arrays marked device
+ * cannot be read by the host, so what they hold is checked by the kernels:
+ * a page outside the pool, a row outside the table or a length beyond the
+ * table's width never leads to an access outside the arrays; what happens
+ * instead is stated at each operator.
+ *
+ * The cache.  Keys and values of one layer are two arrays of num_pages pages
+ *   [kv_heads, page_size, head_dim], contiguous within a page
+ * (page_size a multiple of 16 up to 1024), page p of the keys at
+ * k_cache + p * k_page_stride elements.  block_table[row, b] is the page of
+ * the row's tokens [b * page_size, (b + 1) * page_size), or -1 for none: tokens
+ * without a page (an entry outside [0, num_pages)) are not there, for every
+ * operator.  kv_len[row] counts the row's tokens, the newest included, and is
+ * taken as clamped to [0, max_blocks * page_size].
+ *
+ * Storage types: queries, outputs and new keys and values are BCG_F32 or
+ * BCG_BF16; the cache has the same type, or BCG_E4M3 (OCP float8, 1-4-3)
+ * with BCG_BF16 queries: an element then stands for its value times a scale
+ * of its kv head (device float[kv_heads], positive).
+ */
+#ifndef BCG_DECODE_H
+#define BCG_DECODE_H
+
+#include "bcg.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+enum { BCG_E4M3 = 2 };               /* storage type of a cache, next to BCG_F32, BCG_BF16 */
+
+#define BCG_MAX_HEAD_DIM 256
+#define BCG_MAX_PAGE_SIZE 1024
+#define BCG_MAX_BIASES 4096          /* biases a row in guided_logits */
+
+/*
+ * paged_attention -- one new token a row over its pages.  For query head h of
+ * row r (kv head h / (q_heads / kv_heads)) at position kv_len[r] - 1:
+ *   out = sum_t p_t v_t,  p = softmax_t(scale * q . k_t)
+ * over the row's visible tokens t: those with a page and, when window > 0,
+ * t >= kv_len - window or t < sinks (the newest `window` tokens and the first
+ * `sinks` ones; window == 0: every token).  A row without a visible token
+ * gives zeros, and lse = -infinity.  Tokens that are not visible take no
+ * part, whatever their storage holds (NaN and infinities included).
+ * lse (optional) is the natural log of sum_t exp(scale * q . k_t).
+ * Scores, the softmax and the sums are held in fp32; with a BCG_BF16 query
+ * the probabilities are rounded to bf16 (relative 2^-8 each) before they
+ * weight the values, and out is rounded to nearest even.
+ * A head whose visible scores are all -infinity gives zeros.
+ *
+ * prompt_attention -- the same for runs of new tokens: row r has the queries
+ * [q_offset[r], q_offset[r+1]) of q and out, the last of them at position
+ * kv_len[r] - 1 and the others before it (their keys and values are in the
+ * cache already).  A query at position p sees t <= p and, when window > 0,
+ * t > p - window or t < sinks.  A query at a negative position (a run longer
+ * than kv_len) gives zeros.  Queries that no row has are not written.
+ * q_offset ascends; offsets are taken as clamped to [0, tokens].
+ * A hidden token's storage takes no part, as above.
+ *
+ * workspace: attention_workspace_size(tokens, q_heads, head_dim) bytes,
+ * 16-byte aligned, zero before its first use; every call leaves what the next
+ * one needs.  Calls that may run at the same time need workspaces of their own.
+ * max_len and max_new are upper bounds of kv_len and of a row's new tokens
+ * (they size the launch: tokens beyond them are not seen, queries beyond them
+ * not computed).
+ * out must not overlap anything else.
+ * Errors: BCG_EINVAL (NULL pointer, bad scale, window or sinks negative,
+ * workspace too small, q not a multiple of 16 bytes apart or misaligned),
+ * BCG_ESHAPE (head counts, head_dim not a multiple of 8 -- of 16 for
+ * BCG_E4M3 -- or above BCG_MAX_HEAD_DIM, page size, sizes out of range),
+ * BCG_EDTYPE, BCG_EHIP.
+ */
+typedef struct {
+    int32_t rows;                    /* rows of the block table, >= 0 */
+    int32_t tokens;                  /* query rows of q and out; == rows for paged_attention */
+    int32_t q_heads, kv_heads, head_dim;
+    int32_t page_size, max_blocks, num_pages;
+    int32_t q_dtype, kv_dtype;
+    int32_t max_len;                 /* [0, max_blocks * page_size] */
+    int32_t max_new;                 /* prompt_attention: [0, tokens] (ignored by paged_attention) */
+    int32_t window, sinks;           /* >= 0; window 0: no window, sinks ignored */
+    float scale;                     /* > 0, finite */
+    int32_t reserved;                /* 0 */
+    int64_t q_stride;                /* elements between query rows, >= q_heads * head_dim */
+    int64_t k_page_stride, v_page_stride;  /* elements between pages */
+    const void* q;                   /* device [tokens][q_heads, head_dim] */
+    const void* k_cache;             /* device, as above */
+    const void* v_cache;
+    const int32_t* block_table;      /* device [rows, max_blocks] */
+    const int32_t* kv_len;           /* device [rows] */
+    const int32_t* q_offset;         /* device [rows + 1] (prompt_attention) */
+    const float* k_scale;            /* device [kv_heads] (BCG_E4M3), else NULL */
+    const float* v_scale;
+    void* out;                       /* device [tokens, q_heads, head_dim], contiguous */
+    float* lse;                      /* device [tokens, q_heads] or NULL */
+    void* workspace;
+    size_t workspace_bytes;
+} bcg_attn_args;
+
+size_t attention_workspace_size(int tokens, int q_heads, int head_dim);
+int paged_attention(const bcg_attn_args* args, void* stream);
+int prompt_attention(const bcg_attn_args* args, void* stream);
+
+/*
+ * cache_append -- new keys and values into the pages of one layer: the new
+ * tokens of row r are k, v rows [offset[r], offset[r+1]) (offset NULL: row r's
+ * one token is row r), the last of them at position kv_len[r] - 1.  Tokens at
+ * a negative position or without a page are dropped.  A BCG_E4M3 cache stores
+ * x / scale[head] (fp32), clamped to +-448 and rounded to nearest even; NaN
+ * is stored as 0x7f.  Two rows must not hold the same page where they write.
+ * Errors: as paged_attention; k_stride and v_stride multiples of 16 bytes.
+ */
+typedef struct {
+    int32_t rows, tokens;
+    int32_t kv_heads, head_dim;
+    int32_t page_size, max_blocks, num_pages;
+    int32_t dtype, kv_dtype;
+    int32_t reserved;                /* 0 */
+    int64_t k_stride, v_stride;      /* elements between token rows, >= kv_heads * head_dim */
+    int64_t k_page_stride, v_page_stride;
+    const void* k;                   /* device [tokens][kv_heads, head_dim] */
+    const void* v;
+    const int32_t* offset;           /* device [rows + 1] or NULL (tokens == rows) */
+    const int32_t* block_table;
+    const int32_t* kv_len;
+    const float* k_scale;
+    const float* v_scale;
+    void* k_cache;
+    void* v_cache;
+} bcg_append_args;
+
+int cache_append(const bcg_append_args* args, void* stream);
+
+/*
+ * The pool and its tables.  A pool is `planes` arrays of num_pages pages (the
+ * keys and values of every layer), page p of plane l at
+ * pool + l * plane_stride + p * page_stride bytes, page_bytes long; one block
+ * table serves all planes.  refs[p] counts the table entries that hold page p;
+ * a page with refs <= 0 is free.  A row of length n holds pages in its first
+ * ceil(n / page_size) entries (some may have been given back) and -1 behind
+ * them.  The lists (rows, src, dst, count) are device arrays of n entries.
+ *
+ * cache_extend: row rows[i] grows by count[i] >= 0 tokens; the pages that this
+ *   needs are the lowest free ones, given out in the order of the list and,
+ *   within an entry, of the blocks (refs = 1).  granted[i] = 1, or 0 where
+ *   nothing was changed: a row outside the table, one that an earlier entry of
+ *   the list names, a negative count, a length beyond the table's width, or
+ *   too few free pages (an entry that needs pages fails when the needs up to
+ *   and including it, failed ones counted, exceed the free pages).
+ * cache_fork: row dst[i], which must be empty (length 0, first entry -1),
+ *   becomes a copy of row src[i]: whole pages are shared (refs + 1), a partly
+ *   filled last page that is there is copied to the lowest free page, in list
+ *   order (the forks read the tables as they were before the call).  granted[i] as above (0 also where
+ *   dst[i] is not empty, or equals src[i]).
+ * cache_free: rows[i] gives its pages back (refs - 1 each, its entries -1) and
+ *   has length 0.  With window > 0 it keeps its length, and gives back only
+ *   the pages that hold none of its first `sinks` tokens and none of the
+ *   newest window - 1 (a next token with that window sees no others); a
+ *   partly filled last page stays, the next token goes there.
+ *   Rows outside the table are skipped.
+ * cache_compact: with L live pages (refs > 0), the live pages >= L move, in
+ *   ascending order, into the free pages < L: their data in every plane, their
+ *   refs, and the table entries.  table_out and refs_out may be the inputs
+ *   (in place) or other arrays; entries outside the pool become -1, refs of
+ *   free pages 0.  moved (optional, device int32[1]) is the count of pages.
+ * cache_copy: page src[i] to dst[i] in every plane.  Pairs with a page
+ *   outside the pool are skipped; the dst must be distinct, and no dst a src.
+ *
+ * workspace: cache_workspace_size(rows, num_pages, n) bytes, 16-byte aligned,
+ * any contents; not for calls that run at the same time.
+ * Errors: BCG_EINVAL (NULL pointer, workspace too small, pool or strides not
+ * multiples of 16 bytes, page_bytes > page_stride), BCG_ESHAPE, BCG_EHIP.
+ */
+typedef struct {
+    int32_t planes, num_pages, page_size;
+    int32_t rows, max_blocks;
+    int32_t reserved;                /* 0 */
+    int64_t plane_stride, page_stride, page_bytes;  /* bytes */
+    void* pool;                      /* device */
+    int32_t* block_table;            /* device [rows, max_blocks] */
+    int32_t* kv_len;                 /* device [rows] */
+    int32_t* refs;                   /* device [num_pages] */
+    void* workspace;
+    size_t workspace_bytes;
+} bcg_cache;
+
+size_t cache_workspace_size(int rows, int num_pages, int n);
+int cache_extend(const bcg_cache* cache, int n, const int32_t* rows, const int32_t* count,
+                 int32_t* granted, void* stream);
+int cache_fork(const bcg_cache* cache, int n, const int32_t* src, const int32_t* dst,
+               int32_t* granted, void* stream);
+int cache_free(const bcg_cache* cache, int n, const int32_t* rows, int window, int sinks, void* stream);
+int cache_compact(const bcg_cache* cache, int32_t* table_out, int32_t* refs_out, int32_t* moved,
+                  void* stream);
+int cache_copy(const bcg_cache* cache, int n, const int32_t* src, const int32_t* dst, void* stream);
+
+/*
+ * guided_logits -- the logits that a guided step samples from.  Per sample i
+ * and token j, in fp32 and in this order:
+ *   z = c                          scale[i] == 1, uncond_row[i] < 0 or u == c
+ *   z = fma(scale[i], c - u, u)    otherwise (the combine of guided_step_rows)
+ *   repetition (j in history[i]):  z = z > 0 ? z / rep[i] : z * rep[i]
+ *   frequency, presence:           z = z - freq[i] * m - (m > 0 ? pres[i] : 0)
+ *   bias:                          z = z + bias[i, b], bias_ids[i, b] == j (the last such b)
+ *   temperature:                   z = z / temperature[i]
+ *   grammar mask:                  z = -infinity where bit j of mask[i] is 0
+ * with c = logits[cond_row[i], j], u = logits[uncond_row[i], j] and m the count
+ * of j among the answer's tokens history[i, prompt_len[i] .. history_len[i])
+ * (repetition looks at the prompt's tokens too).  Tokens and ids outside
+ * [0, vocab) are ignored, lengths clamped to [0, max_history], prompt_len NULL
+ * is 0.  A sample whose cond_row is outside [0, logit_rows) is not written; an
+ * uncond_row beyond it counts as -1.  A masked token is -infinity whatever its
+ * logits are; a row whose mask leaves nothing is -infinity throughout.
+ * The penalties, bias, temperature and mask are each optional (NULL).
+ * out must not overlap logits (rows of one may serve several samples).
+ * Errors: BCG_EINVAL (NULL pointer, penalties without a history, bias without
+ * ids, overlap), BCG_ESHAPE, BCG_EDTYPE, BCG_EHIP.
+ */
+typedef struct {
+    int32_t n, vocab, logit_rows;
+    int32_t dtype, out_dtype;        /* BCG_F32 | BCG_BF16 */
+    int32_t max_history, num_biases; /* width of history; of bias_ids and bias */
+    int32_t mask_words;              /* int32 words a row of mask, >= ceil(vocab / 32) */
+    int64_t logit_stride, out_stride;  /* elements between rows, >= vocab */
+    const void* logits;              /* device [logit_rows][vocab] */
+    void* out;                       /* device [n][vocab] */
+    const int32_t* cond_row;         /* device [n] */
+    const int32_t* uncond_row;       /* device [n] or NULL (none) */
+    const float* scale;              /* device [n] (NULL only with uncond_row NULL) */
+    const int32_t* history;          /* device [n, max_history] or NULL */
+    const int32_t* history_len;      /* device [n] */
+    const int32_t* prompt_len;       /* device [n] or NULL */
+    const float* repetition;         /* device [n] or NULL (1) */
+    const float* presence;           /* device [n] or NULL (0) */
+    const float* frequency;          /* device [n] or NULL (0) */
+    const int32_t* bias_ids;         /* device [n, num_biases] or NULL */
+    const float* bias;
+    const float* temperature;        /* device [n] or NULL (1) */
+    const int32_t* mask;             /* device [n, mask_words] or NULL; bit j % 32 of word j / 32 */
+} bcg_logits_args;
+
+int guided_logits(const bcg_logits_args* args, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* BCG_DECODE_H */
