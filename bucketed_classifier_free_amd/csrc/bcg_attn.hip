@@ -13,6 +13,9 @@ extern template hipError_t launch_decode<float, float>(const AttnParams&, hipStr
 extern template hipError_t launch_prompt<bf16_t, bf16_t>(const AttnParams&, hipStream_t);
 extern template hipError_t launch_prompt<bf16_t, e4m3_t>(const AttnParams&, hipStream_t);
 extern template hipError_t launch_prompt<float, float>(const AttnParams&, hipStream_t);
+extern template int prompt_columns<bf16_t, bf16_t>(int);
+extern template int prompt_columns<bf16_t, e4m3_t>(int);
+extern template int prompt_columns<float, float>(int);
 
 namespace {
 
@@ -23,11 +26,11 @@ constexpr int64_t kDecodeGroups = 2048, kPromptGroups = 512;
 constexpr int64_t kMinBlocks = 4;
 
 // (query, head) entries of all splits: splits > 1 only while the groups of one
-// split are below the aim, and a group holds at most 16 (decode) or 128
-// (prompt) entries, so splits * entries < 2 * aim * group.
+// split are below the aim, and a group holds at most 16 (decode) or 256
+// (prompt) entries, so splits * entries < aim * group.
 int64_t max_parts(int64_t entries) {
-    const int64_t cap = 2 * kPromptGroups * 128;
-    static_assert(2 * kPromptGroups * 128 >= 2 * kDecodeGroups * 16, "");
+    const int64_t cap = kPromptGroups * 256;
+    static_assert(kPromptGroups * 256 >= kDecodeGroups * 16, "");
     return entries * kDecodeGroups < cap ? entries * kDecodeGroups : cap;
 }
 
@@ -92,7 +95,10 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     p.window = a->window; p.sinks = a->window > 0 ? a->sinks : 0; p.max_len = a->max_len;
     p.max_new = a->max_new;
     p.scale2 = a->scale * 1.4426950408889634f;
-    const int T = prompt ? 64 : 32, C = prompt ? prompt_columns(a->q_dtype, a->head_dim) : 16;
+    const int T = prompt ? 64 : 32, C = !prompt ? 16
+                                                : a->q_dtype == BCG_F32 ? prompt_columns<float, float>(a->head_dim)
+                                                : a->kv_dtype == BCG_BF16 ? prompt_columns<bf16_t, bf16_t>(a->head_dim)
+                                                                          : prompt_columns<bf16_t, e4m3_t>(a->head_dim);
     const int64_t cols = prompt ? (int64_t)a->max_new * p.G : p.G;
     p.tiles = (int)((cols + C - 1) / C);
     // blocks of the longest list (visible_blocks): all of max_len, or the sinks' and the window's
@@ -129,8 +135,6 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
 }
 
 }  // namespace
-
-int prompt_columns(int, int head_dim) { return 64 * (head_dim > 128 ? 1 : 2); }
 
 }  // namespace bcg
 

@@ -36,7 +36,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr float kNegInf = -__builtin_inff();
-constexpr float kSlack = 8.0f;
+constexpr float kSlack = 8.0f, kMost = 256.0f;  // 2^kSlack
 
 // ---------------------------------------------------------------- operands
 
@@ -202,11 +202,18 @@ __device__ __forceinline__ float col_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
-// The page of the 16 tokens from t on; -1 where there is none.
+// The table's entry for the 16 tokens from t on (-1 at and beyond len), and
+// the page that it names (-1 where there is none).  Two steps, so that an
+// entry can be on its way while something else is done.
+__device__ __forceinline__ int entry_of(const AttnParams& p, const int32_t* row_table, int t, int len) {
+    return t < len ? row_table[p.shift >= 0 ? t >> p.shift : t / p.ps] : -1;
+}
+__device__ __forceinline__ int page_in(const AttnParams& p, int entry) {
+    entry = __builtin_amdgcn_readfirstlane(entry);
+    return entry < p.np ? max(entry, -1) : -1;
+}
 __device__ __forceinline__ int page_of(const AttnParams& p, const int32_t* row_table, int t, int len) {
-    if (t >= len) return -1;
-    const int pg = row_table[p.shift >= 0 ? t >> p.shift : t / p.ps];
-    return pg >= 0 && pg < p.np ? pg : -1;
+    return page_in(p, entry_of(p, row_table, t, len));
 }
 
 template <typename QT, int E>
@@ -373,45 +380,86 @@ __global__ void __launch_bounds__(256) decode_kernel(const AttnParams p) {
 
 // ---------------------------------------------------------------- prompt
 
-// One workgroup: 64 * R columns (query, head of the kv head's group) of one
-// row, four waves of R 16-column tiles each, against 64-token tiles of keys
-// and values that the workgroup stages in LDS in operand order, so that every
-// fragment is one conflict-free 16-byte (fp32: 32-byte) read per lane and
-// serves R products.
-template <typename QT, typename KT, int DP, int R, bool EX> struct Prompt {
-    static constexpr int E = DP / 16, S = DP / 32, T = 64;
-    static constexpr int OW = Op<QT>::dwords;                // dwords of a fragment
+// 16 bytes from each lane's address straight to LDS, lane i's at `to` + 16 i.
+__device__ __forceinline__ void load_lds16(const void* from, unsigned char* to) {
+    __builtin_amdgcn_global_load_lds(from, to, 16, 0, 0);
+}
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+
+// 64 tokens of keys or values in LDS: rows of DP elements as 16-byte chunks,
+// chunk ch of token t in place ch ^ turn(t), so that 16 lanes that read the
+// same chunk of 16 tokens meet all banks.  Written as linear 16-byte slots
+// (what a direct global-to-LDS load does, lane by lane), read as operands.
+template <typename QT, int DP> struct Tile {
     typedef typename Op<QT>::F8 F8;
-    static constexpr int kFrag = 64 * OW;                    // dwords of one fragment, all lanes
-    static constexpr int kSide = T * DP * (int)sizeof(QT) / 4;  // dwords of one tile of keys or values
-    static constexpr int CPR = DP * (int)sizeof(KT) / 16;    // 16-byte chunks of a key
-    static constexpr int KL = T * CPR / 256;                 // chunks a thread stages
-    static constexpr int EPC = 16 / (int)sizeof(KT);         // elements of a chunk
-    static constexpr int VW = E * (int)sizeof(KT) / 4;       // dwords of a thread's part of one value
-
-    struct Stage {
-        Words<4> k[KL];
-        Words<VW> v[4];
-    };
-
-    // Where element block e8 (eight dimensions) of token t lies: fragment
-    // (t / 16, step), lane (c, g), its 16-byte halves rotated by the step and
-    // g so that the lanes that stage one token hit different banks.
-    static __device__ __forceinline__ int k_slot(int t, int e8) {
-        const int s = e8 >> 2, g = e8 & 3;
-        return ((t >> 4) * S + s) * kFrag + (g * 16 + ((t & 15) ^ (e8 & 7))) * OW;
+    static constexpr int T = 64, E = DP / 16, S = DP / 32;
+    static constexpr int RB = DP * (int)sizeof(QT), CH = RB / 16, kBytes = T * RB;
+    static __device__ __forceinline__ int turn(int t) { return CH >= 16 ? t & 15 : (t >> 1) & 7; }
+    static __device__ __forceinline__ int at(int t, int ch) { return t * RB + ((ch ^ turn(t)) << 4); }
+    // the keys of 16-token tile tt, step s: token c, dimensions 32 s + 8 g ..
+    static __device__ __forceinline__ F8 k_frag(const unsigned char* b, int tt, int s, int c, int g) {
+        const int t = tt * 16 + c;
+        if constexpr (sizeof(QT) == 2) {
+            return *reinterpret_cast<const F8*>(b + at(t, s * 4 + g));
+        } else {
+            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(b + at(t, s * 8 + 2 * g));
+            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(b + at(t, s * 8 + 2 * g + 1));
+            return F8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        }
+    }
+    // the values of 32-token block kb, dimension 16 j + c: k index (g, i) as above
+    static __device__ __forceinline__ F8 v_frag(const unsigned char* b, int kb, int j, int c, int g) {
+        if constexpr (sizeof(QT) == 2) {
+            // a transposed read: 16 lanes name four rows of 16 elements, lane c gets column c
+            const int t = kb * 32 + 4 * g + (c >> 2);
+            const unsigned char* a = b + at(t, 2 * j + ((c & 3) >> 1)) + (c & 1) * 8;
+            const i16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)a);
+            const i16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(a + 16 * RB));
+            const u32x2_t u = __builtin_bit_cast(u32x2_t, x), v = __builtin_bit_cast(u32x2_t, y);
+            return F8{u[0], u[1], v[0], v[1]};
+        } else {
+            F8 f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int t = kb * 32 + (i < 4 ? 0 : 16) + 4 * g + (i & 3);
+                f[i] = *reinterpret_cast<const float*>(b + at(t, 4 * j + (c >> 2)) + (c & 3) * 4);
+            }
+            return f;
+        }
     }
 };
 
-template <typename QT, typename KT, int DP, int R, bool EX>
-__global__ void __launch_bounds__(256) prompt_kernel(const AttnParams p) {
-    typedef Prompt<QT, KT, DP, R, EX> P;
-    constexpr int E = P::E, S = P::S, T = P::T, OW = P::OW, C = 64 * R;
+// 16-column tiles of a wave: as many as leave two waves a SIMD their registers
+// (o takes DP/4, the queries' fragments DP/8 (fp32 DP/4) registers each).
+#ifndef KBU
+#define KBU 2
+#endif
+#ifndef MINW
+#define MINW 2
+#endif
+#ifndef R128
+#define R128 2
+#endif
+template <typename QT, int DP> constexpr int prompt_r() {
+    return sizeof(QT) == 2 ? (DP == 64 ? 4 : DP == 128 ? R128 : 1) : (DP == 64 ? 2 : 1);
+}
+
+// One workgroup: 64 * R columns (query, head of the kv head's group) of one
+// row, four waves of R 16-column tiles each, against 64-token tiles of keys
+// and values in LDS.  Each wave stages 16 tokens (one page) of the next tile
+// while all compute on the present one; one barrier a tile.
+template <typename QT, typename KT, int DP, bool EX>
+__global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
+    typedef Tile<QT, DP> L;
+    constexpr int R = prompt_r<QT, DP>(), E = L::E, S = L::S, T = L::T, C = 64 * R, CH = L::CH;
+    constexpr int NB = L::kBytes <= 32768 ? 2 : 1;  // two tiles in flight while LDS holds them
     typedef typename Op<QT>::F8 F8;
-    extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
-    uint32_t* const ks = lds;
-    uint32_t* const vs = lds + P::kSide;
-    int* const odd = reinterpret_cast<int*>(lds + 2 * P::kSide);  // a value that is not finite is in the tile
+    __shared__ __attribute__((aligned(1024))) unsigned char ks0[L::kBytes], vs0[L::kBytes];
+    __shared__ __attribute__((aligned(1024))) unsigned char ks1[NB > 1 ? L::kBytes : 16], vs1[NB > 1 ? L::kBytes : 16];
+    __shared__ __attribute__((aligned(16))) int page0[4], page1[4];  // the pages of the tile's 16-token parts
+    __shared__ int odd;                                              // some value of the tile is not finite
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
 
@@ -429,7 +477,6 @@ __global__ void __launch_bounds__(256) prompt_kernel(const AttnParams p) {
     const int32_t* table = p.table + (int64_t)row * p.maxb;
 
     int pos[R];
-    int64_t at[R];  // (token, head) of this lane's columns, -1: none
     F8 q[R][S];
     const int cw = c0 + wave * 16 * R;
 #pragma unroll
@@ -437,132 +484,146 @@ __global__ void __launch_bounds__(256) prompt_kernel(const AttnParams p) {
         const int col = cw + r * 16 + c, i = col / p.G;
         const bool have = col < cols;
         pos[r] = have ? first + i : -1;
-        const int64_t tok = q0 + i;
         const int head = h * p.G + (col - i * p.G);
-        at[r] = have ? tok * p.qh + head : -1;
-        const QT* qr = static_cast<const QT*>(p.q) + (have ? tok * p.qstride + (int64_t)head * p.D : 0);
+        const QT* qr = static_cast<const QT*>(p.q) + (have ? (int64_t)(q0 + i) * p.qstride + (int64_t)head * p.D : 0);
 #pragma unroll
         for (int s = 0; s < S; ++s) q[r][s] = load_q8<QT>(qr, s * 32 + g * 8, p.D, have);
     }
     // positions of the workgroup's and the wave's queries
     const int pmin = first + c0 / p.G, pmax = first + (min(cols, c0 + C) - 1) / p.G;
-    const bool busy = cw < cols;
-    const int wmax = busy ? first + (min(cols, cw + 16 * R) - 1) / p.G : -1;
+    const int wmax = cw < cols ? first + (min(cols, cw + 16 * R) - 1) / p.G : -1;
     const int lo = p.window > 0 ? max(0, pmin - p.window + 1) : 0;
     const BlockList bl = visible_blocks(lo, pmax + 1, p.sinks, T);
     const int v0 = split * p.chunk, v1 = min(bl.nb, v0 + p.chunk);
 
     const float sc = p.kscale ? p.scale2 * p.kscale[h] : p.scale2;
-    float m[R], nm[R], l[R];
+    const uint32_t span = p.window > 0 ? (uint32_t)p.window : 0x7fffffffu;
+    float m[R], nm[R], lim[R], l[R];  // lim: terms above it move the maximum
     f32x4_t o[R][E];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        m[r] = kNegInf; nm[r] = 0.0f; l[r] = 0.0f;
+        m[r] = kNegInf; nm[r] = 0.0f; lim[r] = -1.0f; l[r] = 0.0f;
 #pragma unroll
         for (int j = 0; j < E; ++j) o[r][j] = f32x4_t{0, 0, 0, 0};
     }
     const KT* kc = static_cast<const KT*>(p.k) + (int64_t)h * p.ps * p.D;
     const KT* vc = static_cast<const KT*>(p.v) + (int64_t)h * p.ps * p.D;
 
-    typename P::Stage st;
-    auto in_page = [&](int t) { return p.shift >= 0 ? t & (p.ps - 1) : t % p.ps; };
-    // what a thread stages: keys as 16-byte chunks, row by row; values as four
-    // tokens (4g'..4g'+3 of a 16-token tile) by E dimensions
-    const int vh = tid >> 6;
-    auto fetch = [&](int vb) {
-        const int t0 = bl(vb) * T;
+    if constexpr (!EX) {
+        // chunks beyond head_dim are never loaded: zero keys there, once
+        for (int i = tid; i < T * CH; i += 256)
+            if ((i % CH ^ L::turn(i / CH)) * (16 / (int)sizeof(QT)) >= p.D) {
+                *reinterpret_cast<u32x4_t*>(ks0 + i * 16) = u32x4_t{0, 0, 0, 0};
+                if constexpr (NB > 1) *reinterpret_cast<u32x4_t*>(ks1 + i * 16) = u32x4_t{0, 0, 0, 0};
+            }
+    }
+
+    // This wave's part of a tile: tokens 16 wave .. 16 wave + 15 of it.  off:
+    // where this lane's chunks lie in the 16 tokens' storage (~0: beyond head_dim).
+    uint32_t off[CH / 4];
+    if constexpr (sizeof(KT) == sizeof(QT)) {
 #pragma unroll
-        for (int i = 0; i < P::KL; ++i) {
-            const int ch = tid + 256 * i, t = ch / P::CPR, d = (ch % P::CPR) * P::EPC;
-            const int half = t0 + (t & ~15);
-            const int pg = page_of(p, table, half, len);
-            const bool in = (EX || d < p.D) && pg >= 0;
-            const KT* a = kc + (int64_t)max(pg, 0) * p.kps + (in_page(half) + (t & 15)) * p.D + (in ? d : 0);
-            const Words<4> x = load_words<4>(a);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) st.k[i].w[w] = EX || d < p.D ? x.w[w] : 0u;
+        for (int i = 0; i < CH / 4; ++i) {
+            const int t = (i * 64 + lane) / CH, d = (lane % CH ^ L::turn(t)) * (16 / (int)sizeof(KT));
+            off[i] = EX || d < p.D ? (uint32_t)(t * p.D + d) * (uint32_t)sizeof(KT) : ~0u;
         }
-        {
-            const int half = t0 + vh * 16, pg = page_of(p, table, half, len);
-            const KT* a = vc + (int64_t)max(pg, 0) * p.vps + (in_page(half) + 4 * g) * p.D;
+    }
+    auto part_entry = [&](int vb) { return vb < v1 ? entry_of(p, table, bl(vb) * T + wave * 16, len) : -1; };
+    auto stage = [&](int vb, int entry, unsigned char* ks, unsigned char* vs, int* page) {
+        const int pg = page_in(p, entry);
+        const int t0 = bl(vb) * T + wave * 16;
+        const int in = p.shift >= 0 ? t0 & (p.ps - 1) : t0 % p.ps;
+        const KT* kr = kc + (int64_t)max(pg, 0) * p.kps + in * p.D;
+        const KT* vr = vc + (int64_t)max(pg, 0) * p.vps + in * p.D;
+        if (lane == 0) page[wave] = pg;
+        if constexpr (sizeof(KT) == sizeof(QT)) {
+            const bool all = pg >= 0 && t0 + 16 <= len;
+            const char* kb = reinterpret_cast<const char*>(kr);
+            const char* vb = reinterpret_cast<const char*>(vr);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                st.v[i] = load_v<KT, E, EX>(a + i * p.D, c * E, p.D);
-                const bool there = (pg >= 0) & (half + 4 * g + i < len);
+            for (int i = 0; i < CH / 4; ++i) {
+                const int slot = (wave * 16 * CH + i * 64) * 16;
+                if (EX || off[i] != ~0u) {
+                    load_lds16(kb + off[i], ks + slot);
+                    if (all) load_lds16(vb + off[i], vs + slot);
+                }
+            }
+            if (!all) {
+                // tokens that are not there have values of zero
 #pragma unroll
-                for (int w = 0; w < P::VW; ++w) st.v[i].w[w] = there ? st.v[i].w[w] : 0u;
+                for (int i = 0; i < CH / 4; ++i) {
+                    const int slot = (wave * 16 * CH + i * 64) * 16;
+                    if (pg < 0 || t0 + (i * 64 + lane) / CH >= len) *reinterpret_cast<u32x4_t*>(vs + slot + lane * 16) = u32x4_t{0, 0, 0, 0};
+                    else if (EX || off[i] != ~0u) load_lds16(vb + off[i], vs + slot);
+                }
+            }
+        } else {
+            // e4m3: 16 elements a lane, widened on the way
+            constexpr int SRC = DP / 16;  // 16-byte chunks of a row
+#pragma unroll
+            for (int i = 0; i < SRC / 4; ++i) {
+                const int x = i * 64 + lane, t = x / SRC, d = x % SRC * 16, tt = wave * 16 + t;
+                if (EX || d < p.D) {
+                    const Words<4> a = load_words<4>(kr + t * p.D + d), b = load_words<4>(vr + t * p.D + d);
+                    const bool there = (pg >= 0) & (t0 + t < len);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        *reinterpret_cast<u32x4_t*>(ks + L::at(tt, d / 8 + e)) =
+                            u32x4_t{e4m3_lo(a.w[2 * e]), e4m3_hi(a.w[2 * e]), e4m3_lo(a.w[2 * e + 1]), e4m3_hi(a.w[2 * e + 1])};
+                        const uint32_t y = there ? b.w[2 * e] : 0u, z = there ? b.w[2 * e + 1] : 0u;
+                        *reinterpret_cast<u32x4_t*>(vs + L::at(tt, d / 8 + e)) = u32x4_t{e4m3_lo(y), e4m3_hi(y), e4m3_lo(z), e4m3_hi(z)};
+                    }
+                }
             }
         }
-    };
-    // not finite: exponent bits all ones (bf16, fp32), or the one NaN code (e4m3)
-    auto strange = [&](uint32_t w) -> bool {
-        if constexpr (sizeof(KT) == 4) return (w & 0x7f800000u) == 0x7f800000u;
-        else if constexpr (sizeof(KT) == 2) return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-        else return (w & 0x7fu) == 0x7fu || (w & 0x7f00u) == 0x7f00u || (w & 0x7f0000u) == 0x7f0000u || (w & 0x7f000000u) == 0x7f000000u;
-    };
-    auto store = [&](bool check) {
-#pragma unroll
-        for (int i = 0; i < P::KL; ++i) {
-            const int ch = tid + 256 * i, t = ch / P::CPR, d = (ch % P::CPR) * P::EPC;
-            const Words<4>& x = st.k[i];
-            if constexpr (sizeof(KT) == 4) {
-                // half of a fragment: dimensions d..d+3
-                *reinterpret_cast<u32x4_t*>(ks + P::k_slot(t, d >> 3) + (d & 4)) = u32x4_t{x.w[0], x.w[1], x.w[2], x.w[3]};
-            } else if constexpr (sizeof(KT) == 2) {
-                *reinterpret_cast<u32x4_t*>(ks + P::k_slot(t, d >> 3)) = u32x4_t{x.w[0], x.w[1], x.w[2], x.w[3]};
-            } else {
-                *reinterpret_cast<u32x4_t*>(ks + P::k_slot(t, d >> 3)) =
-                    u32x4_t{e4m3_lo(x.w[0]), e4m3_hi(x.w[0]), e4m3_lo(x.w[1]), e4m3_hi(x.w[1])};
-                *reinterpret_cast<u32x4_t*>(ks + P::k_slot(t, (d >> 3) + 1)) =
-                    u32x4_t{e4m3_lo(x.w[2]), e4m3_hi(x.w[2]), e4m3_lo(x.w[3]), e4m3_hi(x.w[3])};
-            }
-        }
-        // fragment (two 16-token tiles, dimension j of each lane): the lane's k
-        // indices 0..3 are the first tile's tokens, 4..7 the second's
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            uint32_t* to = vs + ((vh >> 1) * E + j) * P::kFrag + lane * OW + (vh & 1) * (OW / 2);
-            if constexpr (sizeof(KT) == 4) {
-                *reinterpret_cast<u32x4_t*>(to) = u32x4_t{st.v[0].w[j], st.v[1].w[j], st.v[2].w[j], st.v[3].w[j]};
-            } else if constexpr (sizeof(KT) == 2) {
-                const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
-                *reinterpret_cast<u32x2_t*>(to) = u32x2_t{__builtin_amdgcn_perm(st.v[1].w[j >> 1], st.v[0].w[j >> 1], sel),
-                                                          __builtin_amdgcn_perm(st.v[3].w[j >> 1], st.v[2].w[j >> 1], sel)};
-            } else {
-                const uint32_t b = j & 3, sel = 0x0c0c0000u | ((4 + b) << 8) | b;
-                *reinterpret_cast<u32x2_t*>(to) = u32x2_t{e4m3_lo(__builtin_amdgcn_perm(st.v[1].w[j >> 2], st.v[0].w[j >> 2], sel)),
-                                                          e4m3_lo(__builtin_amdgcn_perm(st.v[3].w[j >> 2], st.v[2].w[j >> 2], sel))};
-            }
-        }
-        if (check) {
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int w = 0; w < P::VW; ++w) any = any || strange(st.v[i].w[w]);
-            if (any) *odd = 1;
-        }
-    };
-    auto pages_there = [&](int t0) {
-        bool ok = true;
-#pragma unroll
-        for (int i = 0; i < T / 16; ++i) ok = ok && page_of(p, table, t0 + 16 * i, len) >= 0;
-        return ok;
     };
 
-    if (v0 < v1) fetch(v0);
-    for (int vb = v0; vb < v1; ++vb) {
+    // A tile that every query of the workgroup sees whole needs no masks.
+    auto is_whole = [&](int t0, const int* page) {
+        return t0 + T - 1 <= pmin && (p.window == 0 || t0 > pmax - p.window || t0 + T <= p.sinks) &&
+               (page[0] | page[1] | page[2] | page[3]) >= 0;
+    };
+    auto sees = [&](int t, int r, int page) {
+        return (t <= pos[r]) & ((p.window == 0) | (t > pos[r] - p.window) | (t < p.sinks)) & (page >= 0);
+    };
+    // In a tile that some query sees in part, a value that is not finite is
+    // taken out (0 * it would reach the queries that do not see its token)
+    // and put in at the end, for the queries that see it.
+    // (the exponent's lowest bit added to the exponent alone reaches the sign's
+    // place only from all ones)
+    auto strange = [](uint32_t x) {
+        return sizeof(QT) == 4 ? ((x & 0x7f800000u) + 0x00800000u) & 0x80000000u : ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    };
+    auto clean = [&](unsigned char* vs) {
+        uint32_t any = 0u;
+#pragma unroll
+        for (int k = 0; k < T * CH / 256; ++k) {
+            const int i = k * 256 + tid;
+            if (!EX && (i % CH ^ L::turn(i / CH)) * (16 / (int)sizeof(QT)) >= p.D) continue;
+            const u32x4_t x = *reinterpret_cast<const u32x4_t*>(vs + i * 16);
+            any |= (strange(x[0]) | strange(x[1])) | (strange(x[2]) | strange(x[3]));
+        }
+        if (any) {
+            odd = 1;
+            for (int i = tid; i < T * CH; i += 256) {
+                u32x4_t x = *reinterpret_cast<const u32x4_t*>(vs + i * 16);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t f = strange(x[w]);
+                    if constexpr (sizeof(QT) == 4) x[w] = f ? 0u : x[w];
+                    else x[w] &= (f & 0x80000000u ? 0x0000ffffu : 0xffffffffu) & (f & 0x8000u ? 0xffff0000u : 0xffffffffu);
+                }
+                *reinterpret_cast<u32x4_t*>(vs + i * 16) = x;
+            }
+        }
+        __syncthreads();
+    };
+
+    auto compute = [&](int vb, const unsigned char* ks, unsigned char* vs, const int* page) {
         const int t0 = bl(vb) * T;
-        // a tile that every query of the workgroup sees whole needs no masks
-        const bool whole = t0 + T - 1 <= pmin && (p.window == 0 || t0 > pmax - p.window || t0 + T <= p.sinks) && pages_there(t0);
-        __syncthreads();
-        if (tid == 0) *odd = 0;
-        __syncthreads();
-        store(!whole);
-        __syncthreads();
-        if (vb + 1 < v1) fetch(vb + 1);
-        if (!busy || t0 > wmax) continue;  // nothing here for this wave's queries (the barriers are met above)
-        const bool slow = !whole && *odd;
+        const bool whole = is_whole(t0, page);
+        if (!whole) clean(vs);
+        if (t0 > wmax) return;  // nothing here for this wave's queries
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             f32x4_t x[R][2];
@@ -572,78 +633,136 @@ __global__ void __launch_bounds__(256) prompt_kernel(const AttnParams p) {
             for (int s = 0; s < S; ++s)
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt) {
-                    const F8 a = *reinterpret_cast<const F8*>(ks + ((kb * 2 + tt) * S + s) * P::kFrag + (g * 16 + (c ^ ((s * 4 + g) & 7))) * OW);
+                    const F8 a = L::k_frag(ks, kb * 2 + tt, s, c, g);
 #pragma unroll
                     for (int r = 0; r < R; ++r) Op<QT>::mma(a, q[r][s], x[r][tt]);
                 }
             F8 pf[R];
-            bool seen[R][8];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                x[r][0] *= sc;
-                x[r][1] *= sc;
                 if (!whole) {
-                    const int pg0 = page_of(p, table, t0 + kb * 32, len), pg1 = page_of(p, table, t0 + kb * 32 + 16, len);
+                    const bool rare = t0 < p.sinks || (page[0] | page[1] | page[2] | page[3]) < 0;
+                    const int d = pos[r] - (t0 + kb * 32 + 4 * g);
+                    if (!rare) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int t = t0 + kb * 32 + (i < 4 ? 0 : 16) + 4 * g + (i & 3);
-                        seen[r][i] = (t <= pos[r]) & ((p.window == 0) | (t > pos[r] - p.window) | (t < p.sinks)) & ((i < 4 ? pg0 : pg1) >= 0);
-                        x[r][i >> 2][i & 3] = seen[r][i] ? x[r][i >> 2][i & 3] : kNegInf;
+                        for (int i = 0; i < 8; ++i)  // 0 <= pos - t < span
+                            x[r][i >> 2][i & 3] = (uint32_t)(d - ((i >> 2) * 16 + (i & 3))) < span ? x[r][i >> 2][i & 3] : kNegInf;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int t = t0 + kb * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
+                            x[r][i >> 2][i & 3] = sees(t, r, page[kb * 2 + (i >> 2)]) ? x[r][i >> 2][i & 3] : kNegInf;
+                        }
                     }
                 }
-                const float mx = fmaxf(fmaxf(fmaxf(x[r][0][0], x[r][0][1]), fmaxf(x[r][0][2], x[r][0][3])),
-                                       fmaxf(fmaxf(x[r][1][0], x[r][1][1]), fmaxf(x[r][1][2], x[r][1][3])));
-                if (__any(mx > m[r] + kSlack)) {
+                f32x4_t e[2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i >> 2][i & 3] = exp2_(__builtin_fmaf(x[r][i >> 2][i & 3], sc, nm[r]));
+                const float big = fmaxf(fmaxf(fmaxf(e[0][0], e[0][1]), fmaxf(e[0][2], e[0][3])),
+                                        fmaxf(fmaxf(e[1][0], e[1][1]), fmaxf(e[1][2], e[1][3])));
+                if (__any(big > lim[r])) {
+                    // a term above 2^8, or the query's first ones: move the maximum
+                    const float mx = sc * fmaxf(fmaxf(fmaxf(x[r][0][0], x[r][0][1]), fmaxf(x[r][0][2], x[r][0][3])),
+                                                fmaxf(fmaxf(x[r][1][0], x[r][1][1]), fmaxf(x[r][1][2], x[r][1][3])));
                     const float top = fmaxf(m[r], col_max(mx));
                     const float f = top == kNegInf ? 1.0f : exp2_(m[r] - top);
                     m[r] = top;
                     nm[r] = top == kNegInf ? 0.0f : -top;
+                    lim[r] = top == kNegInf ? -1.0f : kMost;
                     l[r] *= f;
 #pragma unroll
                     for (int j = 0; j < E; ++j) o[r][j] *= f;
-                }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[r][i >> 2][i & 3] = exp2_(x[r][i >> 2][i & 3] + nm[r]);
-                l[r] += ((x[r][0][0] + x[r][0][1]) + (x[r][0][2] + x[r][0][3])) + ((x[r][1][0] + x[r][1][1]) + (x[r][1][2] + x[r][1][3]));
-                pf[r] = Op<QT>::pack(x[r][0], x[r][1]);
+                    for (int i = 0; i < 8; ++i) e[i >> 2][i & 3] = exp2_(__builtin_fmaf(x[r][i >> 2][i & 3], sc, nm[r]));
+                }
+                l[r] += ((e[0][0] + e[0][1]) + (e[0][2] + e[0][3])) + ((e[1][0] + e[1][1]) + (e[1][2] + e[1][3]));
+                pf[r] = Op<QT>::pack(e[0], e[1]);
             }
-            if (!slow) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const F8 a = L::v_frag(vs, kb, j, c, g);
+#pragma unroll
+                for (int r = 0; r < R; ++r) Op<QT>::mma(a, pf[r], o[r][j]);
+            }
+        }
+    };
+
+    if (tid == 0) odd = 0;  // read after the loop's barriers, or this one
+    __syncthreads();
+    int pg = part_entry(v0);
+    if constexpr (NB > 1) {
+        if (v0 < v1) stage(v0, pg, ks0, vs0, page0);
+        pg = part_entry(v0 + 1);
+        for (int vb = v0; vb < v1; vb += 2) {
+            __builtin_amdgcn_s_waitcnt(0);  // this wave's part of the tile has landed
+            __syncthreads();                // all parts have, and nobody reads the other tile any more
+            int next = part_entry(vb + 2);
+            if (vb + 1 < v1) stage(vb + 1, pg, ks1, vs1, page1);
+            compute(vb, ks0, vs0, page0);
+            if (vb + 1 >= v1) break;
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            pg = part_entry(vb + 3);
+            if (vb + 2 < v1) stage(vb + 2, next, ks0, vs0, page0);
+            compute(vb + 1, ks1, vs1, page1);
+        }
+    } else {
+        for (int vb = v0; vb < v1; ++vb) {
+            __syncthreads();
+            stage(vb, pg, ks0, vs0, page0);
+            pg = part_entry(vb + 1);
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            compute(vb, ks0, vs0, page0);
+        }
+    }
+
+    __syncthreads();
+    if (odd) {
+        // Values that are not finite were met: count, for each query and
+        // dimension, the infinities and NaN of the tokens that it sees (1 for
+        // +infinity, 2^10 for -infinity, 2^20 for NaN: at most 32 of each in a
+        // product) and add what they make of the sum.
+        for (int vb = v0; vb < v1; ++vb) {
+            const int t0 = bl(vb) * T;
+            __syncthreads();
+            stage(vb, part_entry(vb), ks0, vs0, page0);
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            if (is_whole(t0, page0)) continue;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                F8 see[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    f32x4_t x[2];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[i >> 2][i & 3] = sees(t0 + kb * 32 + (i < 4 ? 0 : 16) + 4 * g + (i & 3), r, page0[kb * 2 + (i >> 2)]) ? 1.0f : 0.0f;
+                    see[r] = Op<QT>::pack(x[0], x[1]);
+                }
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
-                    const F8 a = *reinterpret_cast<const F8*>(vs + (kb * E + j) * P::kFrag + lane * OW);
+                    const F8 a = L::v_frag(vs0, kb, j, c, g);
+                    f32x4_t w[2];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) Op<QT>::mma(a, pf[r], o[r][j]);
-                }
-            } else {
-                // some value of the tile is not finite: 0 * it must not reach a
-                // query that does not see its token.  One token at a time, each
-                // query taking the sum only if it sees the token.
-                for (int k = 0; k < 32; ++k) {
-                    const int kg = (k >> 2) & 3, ki = (k & 3) + (k >> 4) * 4;  // the k index (g, i) of token k
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t u;
+                        if constexpr (sizeof(QT) == 4) u = __float_as_uint(a[i]);
+                        else u = i & 1 ? a[i >> 1] & 0xffff0000u : a[i >> 1] << 16;
+                        w[i >> 2][i & 3] = (u & 0x7f800000u) != 0x7f800000u ? 0.0f : u == 0x7f800000u ? 1.0f : u == 0xff800000u ? 1024.0f : 1048576.0f;
+                    }
+                    const F8 b = Op<QT>::pack(w[0], w[1]);
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        F8 one = pf[r];
-                        bool mine = false;
+                        f32x4_t y = {0, 0, 0, 0};
+                        Op<QT>::mma(b, see[r], y);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const bool hit = g == kg && i == ki;
-                            mine = mine || (hit && seen[r][i]);
-                            if constexpr (OW == 8) { if (!hit) one[i] = 0.0f; }
-                            else { if (!hit) one[i >> 1] &= i & 1 ? 0x0000ffffu : 0xffff0000u; }
-                        }
-                        mine = __shfl((int)mine, kg * 16 + c) != 0;
-#pragma unroll
-                        for (int j = 0; j < E; ++j) {
-                            F8 a = *reinterpret_cast<const F8*>(vs + (kb * E + j) * P::kFrag + lane * OW);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                if constexpr (OW == 8) { if (!(g == kg && i == ki)) a[i] = 0.0f; }
-                                else { if (!(g == kg && i == ki)) a[i >> 1] &= i & 1 ? 0x0000ffffu : 0xffff0000u; }
-                            }
-                            f32x4_t y = o[r][j];
-                            Op<QT>::mma(a, one, y);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) o[r][j][i] = mine ? y[i] : o[r][j][i];
+                        for (int i = 0; i < 4; ++i) {
+                            const float k = y[i], plus = k - 1024.0f * floorf(k * (1.0f / 1024.0f));
+                            const float nan = __builtin_nanf("");
+                            const float add = k >= 1048576.0f ? nan : (plus > 0.0f ? (k >= 1024.0f ? nan : -kNegInf) : (k >= 1024.0f ? kNegInf : 0.0f));
+                            o[r][j][i] += add;
                         }
                     }
                 }
@@ -655,21 +774,21 @@ __global__ void __launch_bounds__(256) prompt_kernel(const AttnParams p) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const float sum = col_sum(l[r]);
-        if (at[r] < 0) continue;
+        const int col = cw + r * 16 + c, i = col / p.G;
+        if (col >= cols) continue;
+        const int64_t at = (int64_t)(q0 + i) * p.qh + h * p.G + (col - i * p.G);
         const float inv = p.splits > 1 ? vsc : (sum == 0.0f ? 0.0f : vsc / sum);
-        const int64_t to = p.splits > 1 ? (int64_t)split * p.tokens * p.qh + at[r] : at[r];
-        float y[4 * E];
+        const int64_t to = p.splits > 1 ? (int64_t)split * p.tokens * p.qh + at : at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < E; ++j) y[i * E + j] = o[r][j][i] * inv;
+        for (int j = 0; j < E; ++j) {
+            const float y[4] = {o[r][j][0] * inv, o[r][j][1] * inv, o[r][j][2] * inv, o[r][j][3] * inv};
+            if (p.splits == 1) store_row<QT, 4>(static_cast<QT*>(p.out) + to * p.D, y, j * 16 + 4 * g, p.D);
+            else if (v0 < v1) store_row<float, 4>(p.part_o + to * p.D, y, j * 16 + 4 * g, p.D);
+        }
         if (p.splits > 1) {
-            if (v0 < v1) store_row<float, 4 * E>(p.part_o + to * p.D, y, 4 * g * E, p.D);
             if (g == 0) p.part_ml[to] = make_float2(m[r], sum);
-        } else {
-            store_row<QT, 4 * E>(static_cast<QT*>(p.out) + to * p.D, y, 4 * g * E, p.D);
-            if (p.lse && g == 0)
-                p.lse[to] = sum == 0.0f ? kNegInf : (m[r] == kNegInf ? sum : (m[r] + __log2f(sum)) * 0.69314718055994531f);
+        } else if (p.lse && g == 0) {
+            p.lse[to] = sum == 0.0f ? kNegInf : (m[r] == kNegInf ? sum : (m[r] + __log2f(sum)) * 0.69314718055994531f);
         }
     }
 }
@@ -731,27 +850,13 @@ inline hipError_t decode_dp(const AttnParams& p, hipStream_t st) {
     return e != hipSuccess || p.splits == 1 ? e : launch_join<QT>(p, st);
 }
 
-// Tiles of 16 columns a wave takes: as many as the registers hold beside the
-// fragments of the queries.
-template <typename QT, int DP> constexpr int prompt_tiles() { return DP == 256 ? 1 : 2; }
-
-template <typename QT, typename KT, int DP, bool EX>
-inline hipError_t prompt_ex(const AttnParams& p, hipStream_t st) {
-    constexpr int R = prompt_tiles<QT, DP>();
-    constexpr size_t lds = (2 * Prompt<QT, KT, DP, R, EX>::kSide + 4) * sizeof(uint32_t);
-    if constexpr (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prompt_kernel<QT, KT, DP, R, EX>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
-    const dim3 grid((unsigned)((int64_t)p.rows * p.splits * p.kvh * p.tiles));
-    hipLaunchKernelGGL((prompt_kernel<QT, KT, DP, R, EX>), grid, dim3(256), lds, st, p);
-    const hipError_t e = hipGetLastError();
-    return e != hipSuccess || p.splits == 1 ? e : launch_join<QT>(p, st);
-}
 template <typename QT, typename KT, int DP>
 inline hipError_t prompt_dp(const AttnParams& p, hipStream_t st) {
-    return p.D == DP ? prompt_ex<QT, KT, DP, true>(p, st) : prompt_ex<QT, KT, DP, false>(p, st);
+    const dim3 grid((unsigned)((int64_t)p.rows * p.splits * p.kvh * p.tiles));
+    if (p.D == DP) hipLaunchKernelGGL((prompt_kernel<QT, KT, DP, true>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((prompt_kernel<QT, KT, DP, false>), grid, dim3(256), 0, st, p);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || p.splits == 1 ? e : launch_join<QT>(p, st);
 }
 
 }  // namespace attn
@@ -760,6 +865,9 @@ template <typename QT, typename KT> hipError_t launch_decode(const AttnParams& p
     if (p.D <= 64) return attn::decode_dp<QT, KT, 64>(p, st);
     if (p.D <= 128) return attn::decode_dp<QT, KT, 128>(p, st);
     return attn::decode_dp<QT, KT, 256>(p, st);
+}
+template <typename QT, typename KT> int prompt_columns(int D) {
+    return 64 * (D <= 64 ? attn::prompt_r<QT, 64>() : D <= 128 ? attn::prompt_r<QT, 128>() : attn::prompt_r<QT, 256>());
 }
 template <typename QT, typename KT> hipError_t launch_prompt(const AttnParams& p, hipStream_t st) {
     if (p.D <= 64) return attn::prompt_dp<QT, KT, 64>(p, st);
