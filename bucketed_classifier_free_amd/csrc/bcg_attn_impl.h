@@ -624,46 +624,75 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
         const bool whole = is_whole(t0, page);
         if (!whole) clean(vs);
         if (t0 > wmax) return;  // nothing here for this wave's queries
+        // Scores of both 32-token halves first; then, half by half, the terms
+        // of one next to the product of the one before it: matrix and vector
+        // instructions of one wave overlap only within a basic block.
+        f32x4_t x[2][R][2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            f32x4_t x[R][2];
 #pragma unroll
-            for (int r = 0; r < R; ++r) x[r][0] = x[r][1] = f32x4_t{0, 0, 0, 0};
+            for (int r = 0; r < R; ++r) x[kb][r][0] = x[kb][r][1] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int s = 0; s < S; ++s)
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt) {
                     const F8 a = L::k_frag(ks, kb * 2 + tt, s, c, g);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) Op<QT>::mma(a, q[r][s], x[r][tt]);
+                    for (int r = 0; r < R; ++r) Op<QT>::mma(a, q[r][s], x[kb][r][tt]);
                 }
-            F8 pf[R];
+        }
+        if (!whole) {
+            if (t0 >= p.sinks && (page[0] | page[1] | page[2] | page[3]) >= 0) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (!whole) {
-                    const bool rare = t0 < p.sinks || (page[0] | page[1] | page[2] | page[3]) < 0;
-                    const int d = pos[r] - (t0 + kb * 32 + 4 * g);
-                    if (!rare) {
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const int d = pos[r] - (t0 + kb * 32 + 4 * g);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)  // 0 <= pos - t < span
-                            x[r][i >> 2][i & 3] = (uint32_t)(d - ((i >> 2) * 16 + (i & 3))) < span ? x[r][i >> 2][i & 3] : kNegInf;
-                    } else {
+                            x[kb][r][i >> 2][i & 3] = (uint32_t)(d - ((i >> 2) * 16 + (i & 3))) < span ? x[kb][r][i >> 2][i & 3] : kNegInf;
+                    }
+            } else {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int t = t0 + kb * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
-                            x[r][i >> 2][i & 3] = sees(t, r, page[kb * 2 + (i >> 2)]) ? x[r][i >> 2][i & 3] : kNegInf;
+                            x[kb][r][i >> 2][i & 3] = sees(t, r, page[kb * 2 + (i >> 2)]) ? x[kb][r][i >> 2][i & 3] : kNegInf;
                         }
-                    }
-                }
-                f32x4_t e[2];
+            }
+        }
+        F8 pf[R];
+        auto weigh = [&](int kb) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) e[i >> 2][i & 3] = exp2_(__builtin_fmaf(x[r][i >> 2][i & 3], sc, nm[r]));
-                const float big = fmaxf(fmaxf(fmaxf(e[0][0], e[0][1]), fmaxf(e[0][2], e[0][3])),
-                                        fmaxf(fmaxf(e[1][0], e[1][1]), fmaxf(e[1][2], e[1][3])));
-                if (__any(big > lim[r])) {
-                    // a term above 2^8, or the query's first ones: move the maximum
-                    const float mx = sc * fmaxf(fmaxf(fmaxf(x[r][0][0], x[r][0][1]), fmaxf(x[r][0][2], x[r][0][3])),
-                                                fmaxf(fmaxf(x[r][1][0], x[r][1][1]), fmaxf(x[r][1][2], x[r][1][3])));
+            for (int j = 0; j < E; ++j) {
+                const F8 a = L::v_frag(vs, kb, j, c, g);
+#pragma unroll
+                for (int r = 0; r < R; ++r) Op<QT>::mma(a, pf[r], o[r][j]);
+            }
+        };
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            f32x4_t e[R][2];
+            bool move = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[r][i >> 2][i & 3] = exp2_(__builtin_fmaf(x[kb][r][i >> 2][i & 3], sc, nm[r]));
+                const float big = fmaxf(fmaxf(fmaxf(e[r][0][0], e[r][0][1]), fmaxf(e[r][0][2], e[r][0][3])),
+                                        fmaxf(fmaxf(e[r][1][0], e[r][1][1]), fmaxf(e[r][1][2], e[r][1][3])));
+                move = move | (big > lim[r]);
+            }
+            if (kb) weigh(kb - 1);
+            if (__any(move)) {
+                // a term above 2^8, or a query's first ones: move the maximum
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const f32x4_t* y = x[kb][r];
+                    const float mx = sc * fmaxf(fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[0][2], y[0][3])),
+                                                fmaxf(fmaxf(y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3])));
                     const float top = fmaxf(m[r], col_max(mx));
                     const float f = top == kNegInf ? 1.0f : exp2_(m[r] - top);
                     m[r] = top;
@@ -673,18 +702,16 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
 #pragma unroll
                     for (int j = 0; j < E; ++j) o[r][j] *= f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) e[i >> 2][i & 3] = exp2_(__builtin_fmaf(x[r][i >> 2][i & 3], sc, nm[r]));
+                    for (int i = 0; i < 8; ++i) e[r][i >> 2][i & 3] = exp2_(__builtin_fmaf(y[i >> 2][i & 3], sc, nm[r]));
                 }
-                l[r] += ((e[0][0] + e[0][1]) + (e[0][2] + e[0][3])) + ((e[1][0] + e[1][1]) + (e[1][2] + e[1][3]));
-                pf[r] = Op<QT>::pack(e[0], e[1]);
             }
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const F8 a = L::v_frag(vs, kb, j, c, g);
-#pragma unroll
-                for (int r = 0; r < R; ++r) Op<QT>::mma(a, pf[r], o[r][j]);
+            for (int r = 0; r < R; ++r) {
+                l[r] += ((e[r][0][0] + e[r][0][1]) + (e[r][0][2] + e[r][0][3])) + ((e[r][1][0] + e[r][1][1]) + (e[r][1][2] + e[r][1][3]));
+                pf[r] = Op<QT>::pack(e[r][0], e[r][1]);
             }
         }
+        weigh(1);
     };
 
     if (tid == 0) odd = 0;  // read after the loop's barriers, or this one
