@@ -16,6 +16,9 @@ extern template hipError_t launch_prompt<float, float>(const AttnParams&, hipStr
 extern template int prompt_columns<bf16_t, bf16_t>(int);
 extern template int prompt_columns<bf16_t, e4m3_t>(int);
 extern template int prompt_columns<float, float>(int);
+extern template int prompt_block<bf16_t, bf16_t>(int);
+extern template int prompt_block<bf16_t, e4m3_t>(int);
+extern template int prompt_block<float, float>(int);
 
 namespace {
 
@@ -95,10 +98,13 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     p.window = a->window; p.sinks = a->window > 0 ? a->sinks : 0; p.max_len = a->max_len;
     p.max_new = a->max_new;
     p.scale2 = a->scale * 1.4426950408889634f;
-    const int T = prompt ? 64 : 32, C = !prompt ? 16
-                                                : a->q_dtype == BCG_F32 ? prompt_columns<float, float>(a->head_dim)
-                                                : a->kv_dtype == BCG_BF16 ? prompt_columns<bf16_t, bf16_t>(a->head_dim)
-                                                                          : prompt_columns<bf16_t, e4m3_t>(a->head_dim);
+    int T = 32, C = 16;  // tokens of a block, columns of a workgroup
+    if (prompt) {
+        const int D = a->head_dim;
+        if (a->q_dtype == BCG_F32) T = prompt_block<float, float>(D), C = prompt_columns<float, float>(D);
+        else if (a->kv_dtype == BCG_BF16) T = prompt_block<bf16_t, bf16_t>(D), C = prompt_columns<bf16_t, bf16_t>(D);
+        else T = prompt_block<bf16_t, e4m3_t>(D), C = prompt_columns<bf16_t, e4m3_t>(D);
+    }
     const int64_t cols = prompt ? (int64_t)a->max_new * p.G : p.G;
     p.tiles = (int)((cols + C - 1) / C);
     // blocks of the longest list (visible_blocks): all of max_len, or the sinks' and the window's

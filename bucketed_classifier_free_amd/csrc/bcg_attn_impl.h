@@ -388,13 +388,13 @@ __device__ __forceinline__ void load_lds16(const void* from, unsigned char* to) 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 
-// 64 tokens of keys or values in LDS: rows of DP elements as 16-byte chunks,
+// T tokens of keys or values in LDS: rows of DP elements as 16-byte chunks,
 // chunk ch of token t in place ch ^ turn(t), so that 16 lanes that read the
 // same chunk of 16 tokens meet all banks.  Written as linear 16-byte slots
 // (what a direct global-to-LDS load does, lane by lane), read as operands.
-template <typename QT, int DP> struct Tile {
+template <typename QT, int DP, int TT> struct Tile {
     typedef typename Op<QT>::F8 F8;
-    static constexpr int T = 64, E = DP / 16, S = DP / 32;
+    static constexpr int T = TT, E = DP / 16, S = DP / 32;
     static constexpr int RB = DP * (int)sizeof(QT), CH = RB / 16, kBytes = T * RB;
     static __device__ __forceinline__ int turn(int t) { return CH >= 16 ? t & 15 : (t >> 1) & 7; }
     static __device__ __forceinline__ int at(int t, int ch) { return t * RB + ((ch ^ turn(t)) << 4); }
@@ -433,6 +433,22 @@ template <typename QT, int DP> struct Tile {
 
 // 16-column tiles of a wave: as many as leave two waves a SIMD their registers
 // (o takes DP/4, the queries' fragments DP/8 (fp32 DP/4) registers each).
+#ifndef SG
+#define SG 0
+#endif
+#ifndef SGA
+#define SGA 6
+#endif
+#ifndef SGB
+#define SGB 4
+#endif
+#ifndef SGV
+#define SGV 6
+#endif
+#define SCHED(m, n) __builtin_amdgcn_sched_group_barrier(m, n, 0)
+#ifndef PRIO
+#define PRIO 0
+#endif
 #ifndef KBU
 #define KBU 2
 #endif
@@ -442,6 +458,10 @@ template <typename QT, int DP> struct Tile {
 #ifndef R128
 #define R128 2
 #endif
+#ifndef T128
+#define T128 64
+#endif
+template <typename QT, int DP> constexpr int prompt_t() { return sizeof(QT) == 2 && DP == 128 ? T128 : 64; }
 template <typename QT, int DP> constexpr int prompt_r() {
     return sizeof(QT) == 2 ? (DP == 64 ? 4 : DP == 128 ? R128 : 1) : (DP == 64 ? 2 : 1);
 }
@@ -451,15 +471,15 @@ template <typename QT, int DP> constexpr int prompt_r() {
 // and values in LDS.  Each wave stages 16 tokens (one page) of the next tile
 // while all compute on the present one; one barrier a tile.
 template <typename QT, typename KT, int DP, bool EX>
-__global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
-    typedef Tile<QT, DP> L;
+__global__ void __launch_bounds__(256, MINW) prompt_kernel(const AttnParams p) {
+    typedef Tile<QT, DP, prompt_t<QT, DP>()> L;
     constexpr int R = prompt_r<QT, DP>(), E = L::E, S = L::S, T = L::T, C = 64 * R, CH = L::CH;
     constexpr int NB = L::kBytes <= 32768 ? 2 : 1;  // two tiles in flight while LDS holds them
+    constexpr int KB = T / 32, WT = T / 4, NP = T / 16, NL = WT * CH / 64;  // a wave stages WT tokens in NL loads a side
     typedef typename Op<QT>::F8 F8;
     __shared__ __attribute__((aligned(1024))) unsigned char ks0[L::kBytes], vs0[L::kBytes];
     __shared__ __attribute__((aligned(1024))) unsigned char ks1[NB > 1 ? L::kBytes : 16], vs1[NB > 1 ? L::kBytes : 16];
-    __shared__ __attribute__((aligned(16))) int page0[4], page1[4];  // the pages of the tile's 16-token parts
-    __shared__ int odd;                                              // some value of the tile is not finite
+    __shared__ int odd;  // some value was not finite
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
 
@@ -518,31 +538,50 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
             }
     }
 
-    // This wave's part of a tile: tokens 16 wave .. 16 wave + 15 of it.  off:
-    // where this lane's chunks lie in the 16 tokens' storage (~0: beyond head_dim).
-    uint32_t off[CH / 4];
+    // This wave's part of a tile: tokens WT wave .. WT wave + WT - 1 of it.  off:
+    // where this lane's chunks lie in their storage (~0: beyond head_dim).
+    uint32_t off[NL];
     if constexpr (sizeof(KT) == sizeof(QT)) {
 #pragma unroll
-        for (int i = 0; i < CH / 4; ++i) {
-            const int t = (i * 64 + lane) / CH, d = (lane % CH ^ L::turn(t)) * (16 / (int)sizeof(KT));
+        for (int i = 0; i < NL; ++i) {
+            const int t = (i * 64 + lane) / CH, d = ((i * 64 + lane) % CH ^ L::turn(wave * WT + t)) * (16 / (int)sizeof(KT));
             off[i] = EX || d < p.D ? (uint32_t)(t * p.D + d) * (uint32_t)sizeof(KT) : ~0u;
         }
     }
-    auto part_entry = [&](int vb) { return vb < v1 ? entry_of(p, table, bl(vb) * T + wave * 16, len) : -1; };
-    auto stage = [&](int vb, int entry, unsigned char* ks, unsigned char* vs, int* page) {
-        const int pg = page_in(p, entry);
-        const int t0 = bl(vb) * T + wave * 16;
-        const int in = p.shift >= 0 ? t0 & (p.ps - 1) : t0 % p.ps;
+    // Table entries are read for a group of tiles at once, one 16-token part a
+    // lane, and a group ahead: what a tile needs of them is a read of a lane.
+    constexpr int GT = 64 / NP;  // tiles of a group
+    int group_page = -1, group_in = 0, next_page = -1, next_in = 0;  // this lane's part: its page, its place in it
+    uint64_t group_there = 0;                                        // the parts that have a page
+    auto read_group = [&](int vb) {
+        const int v = vb + lane / NP, t = bl(v) * T + lane % NP * 16;
+        next_page = v < v1 && t < len ? table[p.shift >= 0 ? t >> p.shift : t / p.ps] : -1;
+        next_in = p.shift >= 0 ? t & (p.ps - 1) : t % p.ps;
+    };
+    auto turn_group = [&](int vb) {
+        group_page = next_page < p.np ? next_page : -1;
+        group_in = next_in;
+        group_there = __ballot(group_page >= 0);
+        if (vb + GT < v1) read_group(vb + GT);
+    };
+    // Starts tile vb's loads; returns which of its parts have a page.
+    auto stage = [&](int vb, unsigned char* ks, unsigned char* vs) -> uint32_t {
+        const int k = (vb - v0) % GT;
+        if (k == 0) turn_group(vb);
+        const uint32_t there = (uint32_t)(group_there >> k * NP) & ((1u << NP) - 1u);
+        const int part = k * NP + wave * WT / 16;
+        const int pg = __builtin_amdgcn_readlane(group_page, part);
+        const int in = __builtin_amdgcn_readlane(group_in, part) + (wave * WT & 15);
+        const int t0 = bl(vb) * T + wave * WT;
         const KT* kr = kc + (int64_t)max(pg, 0) * p.kps + in * p.D;
         const KT* vr = vc + (int64_t)max(pg, 0) * p.vps + in * p.D;
-        if (lane == 0) page[wave] = pg;
         if constexpr (sizeof(KT) == sizeof(QT)) {
-            const bool all = pg >= 0 && t0 + 16 <= len;
+            const bool all = pg >= 0 && t0 + WT <= len;
             const char* kb = reinterpret_cast<const char*>(kr);
             const char* vb = reinterpret_cast<const char*>(vr);
 #pragma unroll
-            for (int i = 0; i < CH / 4; ++i) {
-                const int slot = (wave * 16 * CH + i * 64) * 16;
+            for (int i = 0; i < NL; ++i) {
+                const int slot = (wave * WT * CH + i * 64) * 16;
                 if (EX || off[i] != ~0u) {
                     load_lds16(kb + off[i], ks + slot);
                     if (all) load_lds16(vb + off[i], vs + slot);
@@ -551,8 +590,8 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
             if (!all) {
                 // tokens that are not there have values of zero
 #pragma unroll
-                for (int i = 0; i < CH / 4; ++i) {
-                    const int slot = (wave * 16 * CH + i * 64) * 16;
+                for (int i = 0; i < NL; ++i) {
+                    const int slot = (wave * WT * CH + i * 64) * 16;
                     if (pg < 0 || t0 + (i * 64 + lane) / CH >= len) *reinterpret_cast<u32x4_t*>(vs + slot + lane * 16) = u32x4_t{0, 0, 0, 0};
                     else if (EX || off[i] != ~0u) load_lds16(vb + off[i], vs + slot);
                 }
@@ -561,9 +600,9 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
             // e4m3: 16 elements a lane, widened on the way
             constexpr int SRC = DP / 16;  // 16-byte chunks of a row
 #pragma unroll
-            for (int i = 0; i < SRC / 4; ++i) {
-                const int x = i * 64 + lane, t = x / SRC, d = x % SRC * 16, tt = wave * 16 + t;
-                if (EX || d < p.D) {
+            for (int i = 0; i < (WT * SRC + 63) / 64; ++i) {
+                const int x = i * 64 + lane, t = x / SRC, d = x % SRC * 16, tt = wave * WT + t;
+                if ((EX || d < p.D) && x < WT * SRC) {
                     const Words<4> a = load_words<4>(kr + t * p.D + d), b = load_words<4>(vr + t * p.D + d);
                     const bool there = (pg >= 0) & (t0 + t < len);
 #pragma unroll
@@ -576,15 +615,16 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
                 }
             }
         }
+        return there;
     };
 
+    constexpr uint32_t kAll = (1u << NP) - 1u;
     // A tile that every query of the workgroup sees whole needs no masks.
-    auto is_whole = [&](int t0, const int* page) {
-        return t0 + T - 1 <= pmin && (p.window == 0 || t0 > pmax - p.window || t0 + T <= p.sinks) &&
-               (page[0] | page[1] | page[2] | page[3]) >= 0;
+    auto is_whole = [&](int t0, uint32_t there) {
+        return t0 + T - 1 <= pmin && (p.window == 0 || t0 > pmax - p.window || t0 + T <= p.sinks) && there == kAll;
     };
-    auto sees = [&](int t, int r, int page) {
-        return (t <= pos[r]) & ((p.window == 0) | (t > pos[r] - p.window) | (t < p.sinks)) & (page >= 0);
+    auto sees = [&](int t, int r, uint32_t there, int part) {
+        return (t <= pos[r]) & ((p.window == 0) | (t > pos[r] - p.window) | (t < p.sinks)) & ((there >> part & 1u) != 0u);
     };
     // In a tile that some query sees in part, a value that is not finite is
     // taken out (0 * it would reach the queries that do not see its token)
@@ -619,17 +659,20 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
         __syncthreads();
     };
 
-    auto compute = [&](int vb, const unsigned char* ks, unsigned char* vs, const int* page) {
+    auto compute = [&](int vb, const unsigned char* ks, unsigned char* vs, uint32_t there) {
         const int t0 = bl(vb) * T;
-        const bool whole = is_whole(t0, page);
+        const bool whole = is_whole(t0, there);
         if (!whole) clean(vs);
         if (t0 > wmax) return;  // nothing here for this wave's queries
-        // Scores of both 32-token halves first; then, half by half, the terms
+        // Scores of all 32-token blocks first; then, block by block, the terms
         // of one next to the product of the one before it: matrix and vector
         // instructions of one wave overlap only within a basic block.
-        f32x4_t x[2][R][2];
+        f32x4_t x[KB][R][2];
+#if PRIO & 1
+        __builtin_amdgcn_s_setprio(1);
+#endif
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+        for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
             for (int r = 0; r < R; ++r) x[kb][r][0] = x[kb][r][1] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
@@ -641,10 +684,21 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
                     for (int r = 0; r < R; ++r) Op<QT>::mma(a, q[r][s], x[kb][r][tt]);
                 }
         }
-        if (!whole) {
-            if (t0 >= p.sinks && (page[0] | page[1] | page[2] | page[3]) >= 0) {
+        if constexpr (sizeof(QT) == 2) {
+#if SG & 1
+            SCHED(0x100, SGA);
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+            for (int i = 0; i < 4 * S - SGA; ++i) { SCHED(0x8, R); SCHED(0x100, 1); }
+            SCHED(0x8, SGA * R);
+#endif
+        }
+#if PRIO & 1
+        __builtin_amdgcn_s_setprio(0);
+#endif
+        if (!whole) {
+            if (t0 >= p.sinks && there == kAll) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         const int d = pos[r] - (t0 + kb * 32 + 4 * g);
@@ -654,13 +708,13 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
                     }
             } else {
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int t = t0 + kb * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
-                            x[kb][r][i >> 2][i & 3] = sees(t, r, page[kb * 2 + (i >> 2)]) ? x[kb][r][i >> 2][i & 3] : kNegInf;
+                            x[kb][r][i >> 2][i & 3] = sees(t, r, there, kb * 2 + (i >> 2)) ? x[kb][r][i >> 2][i & 3] : kNegInf;
                         }
             }
         }
@@ -674,7 +728,7 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
             }
         };
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+        for (int kb = 0; kb < KB; ++kb) {
             f32x4_t e[R][2];
             bool move = false;
 #pragma unroll
@@ -685,7 +739,21 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
                                         fmaxf(fmaxf(e[r][1][0], e[r][1][1]), fmaxf(e[r][1][2], e[r][1][3])));
                 move = move | (big > lim[r]);
             }
-            if (kb) weigh(kb - 1);
+            if (kb) {
+                weigh(kb - 1);
+#if SG & 2
+                if constexpr (sizeof(QT) == 2) {
+                    SCHED(0x100, 2 * SGB);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        SCHED(0x8, R);
+                        SCHED(0x2, SGV);
+                        SCHED(0x400, 2);
+                        if (i < E - SGB) SCHED(0x100, 2);
+                    }
+                }
+#endif
+            }
             if (__any(move)) {
                 // a term above 2^8, or a query's first ones: move the maximum
 #pragma unroll
@@ -711,89 +779,50 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
                 pf[r] = Op<QT>::pack(e[r][0], e[r][1]);
             }
         }
-        weigh(1);
+#if PRIO & 2
+        __builtin_amdgcn_s_setprio(1);
+#endif
+        weigh(KB - 1);
+#if PRIO & 2
+        __builtin_amdgcn_s_setprio(0);
+#endif
+#if SG & 4
+        if constexpr (sizeof(QT) == 2) {
+            SCHED(0x100, 2 * SGB);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                SCHED(0x8, R);
+                SCHED(0x2, 2);
+                if (i < E - SGB) SCHED(0x100, 2);
+            }
+        }
+#endif
     };
 
     if (tid == 0) odd = 0;  // read after the loop's barriers, or this one
     __syncthreads();
-    int pg = part_entry(v0);
+    if (v0 < v1) read_group(v0);
     if constexpr (NB > 1) {
-        if (v0 < v1) stage(v0, pg, ks0, vs0, page0);
-        pg = part_entry(v0 + 1);
+        uint32_t there0 = 0, there1 = 0;
+        if (v0 < v1) there0 = stage(v0, ks0, vs0);
         for (int vb = v0; vb < v1; vb += 2) {
             __builtin_amdgcn_s_waitcnt(0);  // this wave's part of the tile has landed
             __syncthreads();                // all parts have, and nobody reads the other tile any more
-            int next = part_entry(vb + 2);
-            if (vb + 1 < v1) stage(vb + 1, pg, ks1, vs1, page1);
-            compute(vb, ks0, vs0, page0);
+            if (vb + 1 < v1) there1 = stage(vb + 1, ks1, vs1);
+            compute(vb, ks0, vs0, there0);
             if (vb + 1 >= v1) break;
             __builtin_amdgcn_s_waitcnt(0);
             __syncthreads();
-            pg = part_entry(vb + 3);
-            if (vb + 2 < v1) stage(vb + 2, next, ks0, vs0, page0);
-            compute(vb + 1, ks1, vs1, page1);
+            if (vb + 2 < v1) there0 = stage(vb + 2, ks0, vs0);
+            compute(vb + 1, ks1, vs1, there1);
         }
     } else {
         for (int vb = v0; vb < v1; ++vb) {
             __syncthreads();
-            stage(vb, pg, ks0, vs0, page0);
-            pg = part_entry(vb + 1);
+            const uint32_t there = stage(vb, ks0, vs0);
             __builtin_amdgcn_s_waitcnt(0);
             __syncthreads();
-            compute(vb, ks0, vs0, page0);
-        }
-    }
-
-    __syncthreads();
-    if (odd) {
-        // Values that are not finite were met: count, for each query and
-        // dimension, the infinities and NaN of the tokens that it sees (1 for
-        // +infinity, 2^10 for -infinity, 2^20 for NaN: at most 32 of each in a
-        // product) and add what they make of the sum.
-        for (int vb = v0; vb < v1; ++vb) {
-            const int t0 = bl(vb) * T;
-            __syncthreads();
-            stage(vb, part_entry(vb), ks0, vs0, page0);
-            __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();
-            if (is_whole(t0, page0)) continue;
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                F8 see[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    f32x4_t x[2];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i >> 2][i & 3] = sees(t0 + kb * 32 + (i < 4 ? 0 : 16) + 4 * g + (i & 3), r, page0[kb * 2 + (i >> 2)]) ? 1.0f : 0.0f;
-                    see[r] = Op<QT>::pack(x[0], x[1]);
-                }
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const F8 a = L::v_frag(vs0, kb, j, c, g);
-                    f32x4_t w[2];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint32_t u;
-                        if constexpr (sizeof(QT) == 4) u = __float_as_uint(a[i]);
-                        else u = i & 1 ? a[i >> 1] & 0xffff0000u : a[i >> 1] << 16;
-                        w[i >> 2][i & 3] = (u & 0x7f800000u) != 0x7f800000u ? 0.0f : u == 0x7f800000u ? 1.0f : u == 0xff800000u ? 1024.0f : 1048576.0f;
-                    }
-                    const F8 b = Op<QT>::pack(w[0], w[1]);
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        f32x4_t y = {0, 0, 0, 0};
-                        Op<QT>::mma(b, see[r], y);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float k = y[i], plus = k - 1024.0f * floorf(k * (1.0f / 1024.0f));
-                            const float nan = __builtin_nanf("");
-                            const float add = k >= 1048576.0f ? nan : (plus > 0.0f ? (k >= 1024.0f ? nan : -kNegInf) : (k >= 1024.0f ? kNegInf : 0.0f));
-                            o[r][j][i] += add;
-                        }
-                    }
-                }
-            }
+            compute(vb, ks0, vs0, there);
         }
     }
 
@@ -816,6 +845,65 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
             if (g == 0) p.part_ml[to] = make_float2(m[r], sum);
         } else if (p.lse && g == 0) {
             p.lse[to] = sum == 0.0f ? kNegInf : (m[r] == kNegInf ? sum : (m[r] + __log2f(sum)) * 0.69314718055994531f);
+        }
+    }
+
+    __syncthreads();
+    if (odd == 0) return;
+    // Values that are not finite were met: count, for each query and dimension,
+    // the infinities and NaN of the tokens that it sees (1 for +infinity, 2^10
+    // for -infinity, 2^20 for NaN: at most 32 of each in a product) and add
+    // what they make of the sum to what this lane has just stored.
+    read_group(v0);
+    for (int vb = v0; vb < v1; ++vb) {
+        const int t0 = bl(vb) * T;
+        __syncthreads();
+        const uint32_t there = stage(vb, ks0, vs0);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (is_whole(t0, there)) continue;
+#pragma clang loop unroll(disable)
+        for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                f32x4_t x[2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i >> 2][i & 3] = sees(t0 + kb * 32 + (i < 4 ? 0 : 16) + 4 * g + (i & 3), r, there, kb * 2 + (i >> 2)) ? 1.0f : 0.0f;
+                const F8 see = Op<QT>::pack(x[0], x[1]);
+                const int col = cw + r * 16 + c, i = col / p.G;
+                const int64_t at = (int64_t)(q0 + i) * p.qh + h * p.G + (col - i * p.G);
+#pragma clang loop unroll(disable)
+                for (int j = 0; j < E; ++j) {
+                    const F8 a = L::v_frag(vs0, kb, j, c, g);
+                    f32x4_t w[2], y = {0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t u;
+                        if constexpr (sizeof(QT) == 4) u = __float_as_uint(a[i]);
+                        else u = i & 1 ? a[i >> 1] & 0xffff0000u : a[i >> 1] << 16;
+                        w[i >> 2][i & 3] = (u & 0x7f800000u) != 0x7f800000u ? 0.0f : u == 0x7f800000u ? 1.0f : u == 0xff800000u ? 1024.0f : 1048576.0f;
+                    }
+                    Op<QT>::mma(Op<QT>::pack(w[0], w[1]), see, y);
+                    if (col >= cols) continue;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int d = j * 16 + 4 * g + i;
+                        const float plus = y[i] - 1024.0f * floorf(y[i] * (1.0f / 1024.0f));
+                        if (y[i] == 0.0f || d >= p.D) continue;
+                        const float add = y[i] >= 1048576.0f || (plus > 0.0f && y[i] >= 1024.0f) ? __builtin_nanf("") : plus > 0.0f ? -kNegInf : kNegInf;
+                        if (p.splits > 1) {
+                            p.part_o[((int64_t)split * p.tokens * p.qh + at) * p.D + d] += add;
+                        } else {
+                            QT* to = static_cast<QT*>(p.out) + at * p.D + d;
+                            float z[1];
+                            Io<QT, 1>::load(to, z);
+                            z[0] += add;
+                            Io<QT, 1>::store(to, z);
+                        }
+                    }
+                }
+            }
         }
     }
 }
@@ -895,6 +983,9 @@ template <typename QT, typename KT> hipError_t launch_decode(const AttnParams& p
 }
 template <typename QT, typename KT> int prompt_columns(int D) {
     return 64 * (D <= 64 ? attn::prompt_r<QT, 64>() : D <= 128 ? attn::prompt_r<QT, 128>() : attn::prompt_r<QT, 256>());
+}
+template <typename QT, typename KT> int prompt_block(int D) {
+    return D <= 64 ? attn::prompt_t<QT, 64>() : D <= 128 ? attn::prompt_t<QT, 128>() : attn::prompt_t<QT, 256>();
 }
 template <typename QT, typename KT> hipError_t launch_prompt(const AttnParams& p, hipStream_t st) {
     if (p.D <= 64) return attn::prompt_dp<QT, KT, 64>(p, st);
