@@ -9,6 +9,8 @@
 
 namespace bcg {
 
+constexpr int kMaxSplits = 128;
+
 struct AttnParams {
     const void* q;
     const void* k;
@@ -27,6 +29,8 @@ struct AttnParams {
     int ps, shift, maxb, np;    // shift: log2(ps), or -1
     int window, sinks;
     int max_len, max_new, tiles, splits, chunk;  // chunk: blocks of a split
+    int columns;        // prompt: of a workgroup
+    int waves;          // decode: of a workgroup
     float scale2;       // softmax scale * log2(e)
 };
 
@@ -47,9 +51,8 @@ __device__ __forceinline__ BlockList visible_blocks(int lo, int hi, int sinks, i
 
 template <typename QT, typename KT> hipError_t launch_decode(const AttnParams& p, hipStream_t st);
 template <typename QT, typename KT> hipError_t launch_prompt(const AttnParams& p, hipStream_t st);
-// Columns (query, head) of one prompt workgroup, and tokens of its tiles.
+// Columns (query, head) of one prompt workgroup, for runs of many queries.
 template <typename QT, typename KT> int prompt_columns(int head_dim);
-template <typename QT, typename KT> int prompt_block(int head_dim);
 
 struct e4m3_t { uint8_t b; };
 

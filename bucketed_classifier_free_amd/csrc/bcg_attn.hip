@@ -16,17 +16,26 @@ extern template hipError_t launch_prompt<float, float>(const AttnParams&, hipStr
 extern template int prompt_columns<bf16_t, bf16_t>(int);
 extern template int prompt_columns<bf16_t, e4m3_t>(int);
 extern template int prompt_columns<float, float>(int);
-extern template int prompt_block<bf16_t, bf16_t>(int);
-extern template int prompt_block<bf16_t, e4m3_t>(int);
-extern template int prompt_block<float, float>(int);
 
 namespace {
 
-// Workgroups that a decode launch aims at when it splits the rows' tokens (8
+// Workgroups that a decode launch aims at when it splits the rows' tokens (16
 // a CU: rows of unlike lengths even out), and a prompt launch (2 a CU).
-constexpr int64_t kDecodeGroups = 2048, kPromptGroups = 512;
+#ifndef DG
+#define DG 4096
+#endif
+#ifndef NB8
+#define NB8 24
+#endif
+#ifndef LB
+#define LB 64
+#endif
+#ifndef MB
+#define MB 4
+#endif
+constexpr int64_t kDecodeGroups = DG, kPromptGroups = 512;
 // A split is at least this many blocks (decode: 32 tokens, prompt: 64).
-constexpr int64_t kMinBlocks = 4;
+constexpr int64_t kMinBlocks = MB;
 
 // (query, head) entries of all splits: splits > 1 only while the groups of one
 // split are below the aim, and a group holds at most 16 (decode) or 256
@@ -98,14 +107,16 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     p.window = a->window; p.sinks = a->window > 0 ? a->sinks : 0; p.max_len = a->max_len;
     p.max_new = a->max_new;
     p.scale2 = a->scale * 1.4426950408889634f;
-    int T = 32, C = 16;  // tokens of a block, columns of a workgroup
+    const int T = prompt ? 64 : 32;  // tokens of a block
+    int C = 16;                      // columns of a workgroup
+    const int64_t cols = prompt ? (int64_t)a->max_new * p.G : p.G;
     if (prompt) {
         const int D = a->head_dim;
-        if (a->q_dtype == BCG_F32) T = prompt_block<float, float>(D), C = prompt_columns<float, float>(D);
-        else if (a->kv_dtype == BCG_BF16) T = prompt_block<bf16_t, bf16_t>(D), C = prompt_columns<bf16_t, bf16_t>(D);
-        else T = prompt_block<bf16_t, e4m3_t>(D), C = prompt_columns<bf16_t, e4m3_t>(D);
+        C = a->q_dtype == BCG_F32 ? prompt_columns<float, float>(D)
+            : a->kv_dtype == BCG_BF16 ? prompt_columns<bf16_t, bf16_t>(D) : prompt_columns<bf16_t, e4m3_t>(D);
+        if (cols <= 64) C = 64;
     }
-    const int64_t cols = prompt ? (int64_t)a->max_new * p.G : p.G;
+    p.columns = C;
     p.tiles = (int)((cols + C - 1) / C);
     // blocks of the longest list (visible_blocks): all of max_len, or the sinks' and the window's
     int64_t nb = ((int64_t)a->max_len + T - 1) / T;
@@ -118,6 +129,14 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     const int64_t groups = (int64_t)(prompt ? (a->tokens * (int64_t)p.G + C - 1) / C + a->rows : (int64_t)a->rows * p.tiles) * p.kvh;
     const int64_t aim = prompt ? kPromptGroups : kDecodeGroups;
     int64_t splits = groups >= aim ? 1 : aim / groups;
+    if (!prompt) {
+        // half of the aim is enough where the splits would get shorter than 64 blocks
+        const int64_t lng = nb / LB > aim / 2 / groups ? nb / LB : aim / 2 / groups;
+        if (splits > lng) splits = lng < 1 ? 1 : lng;
+        // short rows: eight waves, and no second launch to join splits
+        if (nb <= NB8 && groups < 1024 && a->q_dtype == BCG_BF16 && a->head_dim <= 128) splits = 1, p.waves = 8;
+    }
+    if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits > (nb + kMinBlocks - 1) / kMinBlocks) splits = (nb + kMinBlocks - 1) / kMinBlocks;
     p.chunk = (int)((nb + splits - 1) / splits);
     p.splits = (int)((nb + p.chunk - 1) / p.chunk);

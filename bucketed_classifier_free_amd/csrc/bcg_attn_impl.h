@@ -202,25 +202,18 @@ __device__ __forceinline__ float col_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
-// The table's entry for the 16 tokens from t on (-1 at and beyond len), and
-// the page that it names (-1 where there is none).  Two steps, so that an
-// entry can be on its way while something else is done.
-__device__ __forceinline__ int entry_of(const AttnParams& p, const int32_t* row_table, int t, int len) {
-    return t < len ? row_table[p.shift >= 0 ? t >> p.shift : t / p.ps] : -1;
-}
-__device__ __forceinline__ int page_in(const AttnParams& p, int entry) {
-    entry = __builtin_amdgcn_readfirstlane(entry);
-    return entry < p.np ? max(entry, -1) : -1;
-}
-__device__ __forceinline__ int page_of(const AttnParams& p, const int32_t* row_table, int t, int len) {
-    return page_in(p, entry_of(p, row_table, t, len));
-}
-
 template <typename QT, int E>
 __device__ __forceinline__ void store_row(QT* out, const float (&x)[E], int d, int D) {
-    // D is a multiple of 8 and E of 4: groups of four are stored or left out whole
+    // D is a multiple of 8 and E of 4 (or 2): groups are stored or left out whole
+    if constexpr (E == 2) {
+        if (d < D) {
+            if constexpr (sizeof(QT) == 4) *reinterpret_cast<float2*>(out + d) = make_float2(x[0], x[1]);
+            else *reinterpret_cast<uint32_t*>(out + d) = pack_bf16x2(x[0], x[1]);
+        }
+        return;
+    }
 #pragma unroll
-    for (int i = 0; i < E; i += 4) {
+    for (int i = 0; i + 4 <= E; i += 4) {
         if (d + i < D) {
             if constexpr (sizeof(QT) == 4) {
                 *reinterpret_cast<f32x4_t*>(out + d + i) = f32x4_t{x[i], x[i + 1], x[i + 2], x[i + 3]};
@@ -231,25 +224,80 @@ __device__ __forceinline__ void store_row(QT* out, const float (&x)[E], int d, i
     }
 }
 
+// ---------------------------------------------------------------- join
+
+// One wave a (token, head): out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
+// Lane s holds the weight of split s (and s + 64); the splits' rows are then
+// read 64 / LR at a time (LR lanes of four dimensions a row), four loads in flight.
+template <typename QT, int DP> __device__ __forceinline__ void join_splits(const AttnParams& p, int64_t at) {
+    constexpr int LR = DP / 4, NG = 64 / LR;
+    const int64_t n = (int64_t)p.tokens * p.qh;
+    const int lane = threadIdx.x & 63;
+    float2 ml[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        ml[k] = lane + 64 * k < p.splits ? p.part_ml[(lane + 64 * k) * n + at] : make_float2(kNegInf, 0.0f);
+    float top = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+    // nothing seen in a split (m = -infinity, l = 0): its o was not written; l = NaN without a maximum: NaN scores
+    float w[2], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const bool none = ml[k].x == kNegInf;
+        w[k] = none ? (ml[k].y == 0.0f ? 0.0f : 1.0f) : exp2_(ml[k].x - top);
+        sum += w[k] == 0.0f ? 0.0f : w[k] * ml[k].y;
+    }
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k);
+    const int d = lane % LR * 4, sub = lane / LR;
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float* po = p.part_o + at * p.D + (d < p.D ? d : 0);
+    for (int s0 = 0; s0 < p.splits; s0 += 4 * NG) {
+        f32x4_t y[4];
+        float f[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int s = s0 + u * NG + sub;
+            const float fa = __shfl(w[0], s & 63), fb = __shfl(w[1], s & 63);
+            f[u] = s < p.splits ? (s < 64 ? fa : fb) : 0.0f;
+            y[u] = f32x4_t{0, 0, 0, 0};
+            if (f[u] != 0.0f) y[u] = *reinterpret_cast<const f32x4_t*>(po + s * n * p.D);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] += f[u] * y[u][i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int k = LR; k < 64; k <<= 1) x[i] += __shfl_xor(x[i], k);
+        x[i] = sum == 0.0f ? 0.0f : x[i] / sum;
+    }
+    if (sub == 0) store_row<QT, 4>(static_cast<QT*>(p.out) + at * p.D, x, d, p.D);
+    if (p.lse && lane == 0)
+        p.lse[at] = sum == 0.0f ? kNegInf : (top == kNegInf ? sum : (top + __log2f(sum)) * 0.69314718055994531f);
+}
+
 // ---------------------------------------------------------------- decode
 
 // One workgroup: the tokens of one split of a row for up to 16 query heads of
-// one kv head.  Four waves take the split's 32-token blocks in turn, straight
+// one kv head.  NW waves take the split's 32-token blocks in turn, straight
 // from memory into registers (each key and value is used once, so there is
 // nothing for LDS to share); their states are joined in LDS at the end.
-template <typename QT, typename KT, int DP, bool EX>
-__global__ void __launch_bounds__(256) decode_kernel(const AttnParams p) {
+template <typename QT, typename KT, int DP, int NW, bool EX>
+__global__ void __launch_bounds__(64 * NW) decode_kernel(const AttnParams p) {
     constexpr int E = DP / 16, S = DP / 32;
     typedef typename Op<QT>::F8 F8;
-    __shared__ float2 ml_s[4][16];
-    __shared__ __attribute__((aligned(16))) float o_s[4][16][DP];
+    __shared__ float2 ml_s[NW][16];
+    __shared__ __attribute__((aligned(16))) float o_s[NW][16][DP];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     unsigned id = blockIdx.x;
     const int tile = id % p.tiles; id /= p.tiles;
     const int h = id % p.kvh; id /= p.kvh;
-    const int split = id % p.splits;
-    const int row = id / p.splits;
+    const int row = id % p.rows, split = id / p.rows;  // short rows' empty splits come last, not every few groups
     const int len = min(max(p.len[row], 0), p.max_len);
     const int lo = p.window > 0 ? max(0, len - p.window) : 0;
     const BlockList bl = visible_blocks(lo, len, p.sinks, 32);
@@ -271,11 +319,24 @@ __global__ void __launch_bounds__(256) decode_kernel(const AttnParams p) {
     const KT* kc = static_cast<const KT*>(p.k) + (int64_t)h * p.ps * p.D;
     const KT* vc = static_cast<const KT*>(p.v) + (int64_t)h * p.ps * p.D;
 
-    for (int vb = v0 + wave; vb < v1; vb += 4) {
+    // Table entries are read 32 blocks at a time, one 16-token part a lane, and
+    // a group ahead: a block's pages are then two reads of a lane.
+    int part_page = -1, part_in = 0, next_page = -1, next_in = 0;
+    auto read_group = [&](int vb) {
+        const int v = vb + (lane >> 1) * NW, t = bl(v) * 32 + (lane & 1) * 16;
+        next_page = v < v1 && t < len ? table[p.shift >= 0 ? t >> p.shift : t / p.ps] : -1;
+        next_in = p.shift >= 0 ? t & (p.ps - 1) : t % p.ps;
+    };
+    if (v0 + wave < v1) read_group(v0 + wave);
+    for (int vb = v0 + wave, n = 0; vb < v1; vb += NW, ++n) {
+        if ((n & 31) == 0) {
+            part_page = next_page < p.np ? next_page : -1;
+            part_in = next_in;
+            if (vb + 32 * NW < v1) read_group(vb + 32 * NW);
+        }
         const int t0 = bl(vb) * 32;
-        const int pg0 = page_of(p, table, t0, len), pg1 = page_of(p, table, t0 + 16, len);
-        const int in0 = p.shift >= 0 ? t0 & (p.ps - 1) : t0 % p.ps;
-        const int in1 = p.shift >= 0 ? (t0 + 16) & (p.ps - 1) : (t0 + 16) % p.ps;
+        const int pg0 = __builtin_amdgcn_readlane(part_page, 2 * (n & 31)), pg1 = __builtin_amdgcn_readlane(part_page, 2 * (n & 31) + 1);
+        const int in0 = __builtin_amdgcn_readlane(part_in, 2 * (n & 31)), in1 = __builtin_amdgcn_readlane(part_in, 2 * (n & 31) + 1);
         const int64_t a0 = max(pg0, 0), a1 = max(pg1, 0);
         KTile<KT, DP, EX> k0, k1;
         k0.load(kc + a0 * p.kps + (in0 + c) * p.D, g, p.D);
@@ -333,14 +394,14 @@ __global__ void __launch_bounds__(256) decode_kernel(const AttnParams p) {
         for (int j = 0; j < E; ++j) Op<QT>::mma(v_frag<QT, KT, E>(v, j), pf, o[j]);
     }
 
-    // join the four waves
+    // join the waves
     l = col_sum(l);
     if (g == 0) ml_s[wave][c] = make_float2(m, l);
     __syncthreads();
     {
         float top = kNegInf;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, ml_s[w][c].x);
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, ml_s[w][c].x);
         // m = -infinity: nothing seen (l and o are 0), or nothing but NaN scores (they are NaN)
         const float f = m == kNegInf ? 1.0f : exp2_(m - top);
 #pragma unroll
@@ -349,32 +410,38 @@ __global__ void __launch_bounds__(256) decode_kernel(const AttnParams p) {
             for (int j = 0; j < E; ++j) o_s[wave][c][(4 * g + i) * E + j] = o[j][i] * f;
     }
     __syncthreads();
-    const int hh = threadIdx.x >> 4, d = (threadIdx.x & 15) * E;
-    if (hh >= nh) return;
-    float top = kNegInf, sum = 0.0f;
+    constexpr int EO = 4 * E / NW;  // dimensions of a lane
+    const int hh = threadIdx.x / (DP / EO), d = threadIdx.x % (DP / EO) * EO;
+    if (hh < nh) {
+        float top = kNegInf, sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml_s[w][hh].x);
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, ml_s[w][hh].x);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) sum += ml_s[w][hh].x == kNegInf ? ml_s[w][hh].y : ml_s[w][hh].y * exp2_(ml_s[w][hh].x - top);
-    float x[E];
+        for (int w = 0; w < NW; ++w) sum += ml_s[w][hh].x == kNegInf ? ml_s[w][hh].y : ml_s[w][hh].y * exp2_(ml_s[w][hh].x - top);
+        float x[EO];
 #pragma unroll
-    for (int j = 0; j < E; ++j) x[j] = (o_s[0][hh][d + j] + o_s[1][hh][d + j]) + (o_s[2][hh][d + j] + o_s[3][hh][d + j]);
-    const int64_t at = (int64_t)row * p.qh + head0 + hh;
-    const float vs = p.vscale ? p.vscale[h] : 1.0f;
-    if (p.splits == 1) {
-        const float inv = sum == 0.0f ? 0.0f : vs / sum;
+        for (int j = 0; j < EO; ++j) {
+            x[j] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < E; ++j) x[j] *= inv;
-        store_row<QT, E>(static_cast<QT*>(p.out) + at * p.D, x, d, p.D);
-        if (p.lse && d == 0) p.lse[at] = sum == 0.0f ? kNegInf : (top == kNegInf ? sum : (top + __log2f(sum)) * 0.69314718055994531f);
-    } else {
-        const int64_t ps = (int64_t)split * p.tokens * p.qh + at;
-        if (v0 < v1) {
-#pragma unroll
-            for (int j = 0; j < E; ++j) x[j] *= vs;
-            store_row<float, E>(p.part_o + ps * p.D, x, d, p.D);
+            for (int w = 0; w < NW; ++w) x[j] += o_s[w][hh][d + j];
         }
-        if (d == 0) p.part_ml[ps] = make_float2(top, sum);
+        const int64_t at = (int64_t)row * p.qh + head0 + hh;
+        const float vs = p.vscale ? p.vscale[h] : 1.0f;
+        if (p.splits == 1) {
+            const float inv = sum == 0.0f ? 0.0f : vs / sum;
+#pragma unroll
+            for (int j = 0; j < EO; ++j) x[j] *= inv;
+            store_row<QT, EO>(static_cast<QT*>(p.out) + at * p.D, x, d, p.D);
+            if (p.lse && d == 0) p.lse[at] = sum == 0.0f ? kNegInf : (top == kNegInf ? sum : (top + __log2f(sum)) * 0.69314718055994531f);
+        } else {
+            const int64_t ps = (int64_t)split * p.tokens * p.qh + at;
+            if (v0 < v1) {
+#pragma unroll
+                for (int j = 0; j < EO; ++j) x[j] *= vs;
+                store_row<float, EO>(p.part_o + ps * p.D, x, d, p.D);
+            }
+            if (d == 0) p.part_ml[ps] = make_float2(top, sum);
+        }
     }
 }
 
@@ -431,49 +498,20 @@ template <typename QT, int DP, int TT> struct Tile {
     }
 };
 
-// 16-column tiles of a wave: as many as leave two waves a SIMD their registers
-// (o takes DP/4, the queries' fragments DP/8 (fp32 DP/4) registers each).
-#ifndef SG
-#define SG 0
-#endif
-#ifndef SGA
-#define SGA 6
-#endif
-#ifndef SGB
-#define SGB 4
-#endif
-#ifndef SGV
-#define SGV 6
-#endif
-#define SCHED(m, n) __builtin_amdgcn_sched_group_barrier(m, n, 0)
-#ifndef PRIO
-#define PRIO 0
-#endif
-#ifndef KBU
-#define KBU 2
-#endif
-#ifndef MINW
-#define MINW 2
-#endif
-#ifndef R128
-#define R128 2
-#endif
-#ifndef T128
-#define T128 64
-#endif
-template <typename QT, int DP> constexpr int prompt_t() { return sizeof(QT) == 2 && DP == 128 ? T128 : 64; }
-template <typename QT, int DP> constexpr int prompt_r() {
-    return sizeof(QT) == 2 ? (DP == 64 ? 4 : DP == 128 ? R128 : 1) : (DP == 64 ? 2 : 1);
-}
+// 16-column tiles of a wave for runs of many queries: as many as leave two
+// waves a SIMD their registers (o takes DP/4, the queries' fragments DP/8
+// registers each), since every fragment that is read from LDS serves so many
+// products.  In fp32 a product takes 16 times as long and one tile is enough.
+template <typename QT, int DP> constexpr int prompt_r() { return sizeof(QT) == 4 || DP == 256 ? 1 : DP == 128 ? 2 : 3; }
 
 // One workgroup: 64 * R columns (query, head of the kv head's group) of one
 // row, four waves of R 16-column tiles each, against 64-token tiles of keys
 // and values in LDS.  Each wave stages 16 tokens (one page) of the next tile
 // while all compute on the present one; one barrier a tile.
-template <typename QT, typename KT, int DP, bool EX>
-__global__ void __launch_bounds__(256, MINW) prompt_kernel(const AttnParams p) {
-    typedef Tile<QT, DP, prompt_t<QT, DP>()> L;
-    constexpr int R = prompt_r<QT, DP>(), E = L::E, S = L::S, T = L::T, C = 64 * R, CH = L::CH;
+template <typename QT, typename KT, int DP, int R, bool EX>
+__global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
+    typedef Tile<QT, DP, 64> L;
+    constexpr int E = L::E, S = L::S, T = L::T, C = 64 * R, CH = L::CH;
     constexpr int NB = L::kBytes <= 32768 ? 2 : 1;  // two tiles in flight while LDS holds them
     constexpr int KB = T / 32, WT = T / 4, NP = T / 16, NL = WT * CH / 64;  // a wave stages WT tokens in NL loads a side
     typedef typename Op<QT>::F8 F8;
@@ -668,9 +706,6 @@ __global__ void __launch_bounds__(256, MINW) prompt_kernel(const AttnParams p) {
         // of one next to the product of the one before it: matrix and vector
         // instructions of one wave overlap only within a basic block.
         f32x4_t x[KB][R][2];
-#if PRIO & 1
-        __builtin_amdgcn_s_setprio(1);
-#endif
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
@@ -684,17 +719,6 @@ __global__ void __launch_bounds__(256, MINW) prompt_kernel(const AttnParams p) {
                     for (int r = 0; r < R; ++r) Op<QT>::mma(a, q[r][s], x[kb][r][tt]);
                 }
         }
-        if constexpr (sizeof(QT) == 2) {
-#if SG & 1
-            SCHED(0x100, SGA);
-#pragma unroll
-            for (int i = 0; i < 4 * S - SGA; ++i) { SCHED(0x8, R); SCHED(0x100, 1); }
-            SCHED(0x8, SGA * R);
-#endif
-        }
-#if PRIO & 1
-        __builtin_amdgcn_s_setprio(0);
-#endif
         if (!whole) {
             if (t0 >= p.sinks && there == kAll) {
 #pragma unroll
@@ -739,21 +763,7 @@ __global__ void __launch_bounds__(256, MINW) prompt_kernel(const AttnParams p) {
                                         fmaxf(fmaxf(e[r][1][0], e[r][1][1]), fmaxf(e[r][1][2], e[r][1][3])));
                 move = move | (big > lim[r]);
             }
-            if (kb) {
-                weigh(kb - 1);
-#if SG & 2
-                if constexpr (sizeof(QT) == 2) {
-                    SCHED(0x100, 2 * SGB);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        SCHED(0x8, R);
-                        SCHED(0x2, SGV);
-                        SCHED(0x400, 2);
-                        if (i < E - SGB) SCHED(0x100, 2);
-                    }
-                }
-#endif
-            }
+            if (kb) weigh(kb - 1);
             if (__any(move)) {
                 // a term above 2^8, or a query's first ones: move the maximum
 #pragma unroll
@@ -779,24 +789,7 @@ __global__ void __launch_bounds__(256, MINW) prompt_kernel(const AttnParams p) {
                 pf[r] = Op<QT>::pack(e[r][0], e[r][1]);
             }
         }
-#if PRIO & 2
-        __builtin_amdgcn_s_setprio(1);
-#endif
         weigh(KB - 1);
-#if PRIO & 2
-        __builtin_amdgcn_s_setprio(0);
-#endif
-#if SG & 4
-        if constexpr (sizeof(QT) == 2) {
-            SCHED(0x100, 2 * SGB);
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                SCHED(0x8, R);
-                SCHED(0x2, 2);
-                if (i < E - SGB) SCHED(0x100, 2);
-            }
-        }
-#endif
     };
 
     if (tid == 0) odd = 0;  // read after the loop's barriers, or this one
@@ -908,13 +901,11 @@ __global__ void __launch_bounds__(256, MINW) prompt_kernel(const AttnParams p) {
     }
 }
 
-// ---------------------------------------------------------------- join
 
-// One wave a (token, head): out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
-template <typename QT> __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
-    const int64_t n = (int64_t)p.tokens * p.qh, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+template <typename QT, int DP> __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    if (at >= n) return;
+    if (at >= (int64_t)p.tokens * p.qh) return;
     if (p.qoff) {
         // a token that no row has, or beyond max_new, was not computed
         const int tok = (int)(at / p.qh);
@@ -925,53 +916,41 @@ template <typename QT> __global__ void __launch_bounds__(256) join_kernel(const 
         }
         if (!__any(mine)) return;
     }
-    float top = kNegInf;
-    for (int s = lane; s < p.splits; s += 64) top = fmaxf(top, p.part_ml[s * n + at].x);
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
-    float sum = 0.0f, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int d = lane * 4;
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 ml = p.part_ml[s * n + at];
-        if (ml.x == kNegInf && ml.y == 0.0f) continue;  // nothing seen there, its o is not written
-        const float f = ml.x == kNegInf ? 1.0f : exp2_(ml.x - top);
-        sum += f * ml.y;
-        if (d < p.D) {
-            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(p.part_o + (s * n + at) * p.D + d);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] += f * y[i];
-        }
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] *= inv;
-    store_row<QT, 4>(static_cast<QT*>(p.out) + at * p.D, x, d, p.D);
-    if (p.lse && lane == 0)
-        p.lse[at] = sum == 0.0f ? kNegInf : (top == kNegInf ? sum : (top + __log2f(sum)) * 0.69314718055994531f);
+    join_splits<QT, DP>(p, at);
 }
 
-template <typename QT> inline hipError_t launch_join(const AttnParams& p, hipStream_t st) {
+template <typename QT, int DP> inline hipError_t launch_join(const AttnParams& p, hipStream_t st) {
     const int64_t n = (int64_t)p.tokens * p.qh;
-    hipLaunchKernelGGL((join_kernel<QT>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, p);
+    hipLaunchKernelGGL((join_kernel<QT, DP>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 
 template <typename QT, typename KT, int DP>
 inline hipError_t decode_dp(const AttnParams& p, hipStream_t st) {
     const dim3 grid((unsigned)((int64_t)p.rows * p.splits * p.kvh * p.tiles));
-    if (p.D == DP) hipLaunchKernelGGL((decode_kernel<QT, KT, DP, true>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((decode_kernel<QT, KT, DP, false>), grid, dim3(256), 0, st, p);
+    if (p.waves == 8) {
+        if (p.D == DP) hipLaunchKernelGGL((decode_kernel<QT, KT, DP, 8, true>), grid, dim3(512), 0, st, p);
+        else hipLaunchKernelGGL((decode_kernel<QT, KT, DP, 8, false>), grid, dim3(512), 0, st, p);
+    } else {
+        if (p.D == DP) hipLaunchKernelGGL((decode_kernel<QT, KT, DP, 4, true>), grid, dim3(256), 0, st, p);
+        else hipLaunchKernelGGL((decode_kernel<QT, KT, DP, 4, false>), grid, dim3(256), 0, st, p);
+    }
     const hipError_t e = hipGetLastError();
-    return e != hipSuccess || p.splits == 1 ? e : launch_join<QT>(p, st);
+    return e != hipSuccess || p.splits == 1 ? e : launch_join<QT, DP>(p, st);
 }
 
+template <typename QT, typename KT, int DP, int R>
+inline void prompt_r_launch(const AttnParams& p, hipStream_t st) {
+    const dim3 grid((unsigned)((int64_t)p.rows * p.splits * p.kvh * p.tiles));
+    if (p.D == DP) hipLaunchKernelGGL((prompt_kernel<QT, KT, DP, R, true>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((prompt_kernel<QT, KT, DP, R, false>), grid, dim3(256), 0, st, p);
+}
 template <typename QT, typename KT, int DP>
 inline hipError_t prompt_dp(const AttnParams& p, hipStream_t st) {
-    const dim3 grid((unsigned)((int64_t)p.rows * p.splits * p.kvh * p.tiles));
-    if (p.D == DP) hipLaunchKernelGGL((prompt_kernel<QT, KT, DP, true>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((prompt_kernel<QT, KT, DP, false>), grid, dim3(256), 0, st, p);
+    if (p.columns == 64) prompt_r_launch<QT, KT, DP, 1>(p, st);
+    else prompt_r_launch<QT, KT, DP, prompt_r<QT, DP>()>(p, st);
     const hipError_t e = hipGetLastError();
-    return e != hipSuccess || p.splits == 1 ? e : launch_join<QT>(p, st);
+    return e != hipSuccess || p.splits == 1 ? e : launch_join<QT, DP>(p, st);
 }
 
 }  // namespace attn
@@ -983,9 +962,6 @@ template <typename QT, typename KT> hipError_t launch_decode(const AttnParams& p
 }
 template <typename QT, typename KT> int prompt_columns(int D) {
     return 64 * (D <= 64 ? attn::prompt_r<QT, 64>() : D <= 128 ? attn::prompt_r<QT, 128>() : attn::prompt_r<QT, 256>());
-}
-template <typename QT, typename KT> int prompt_block(int D) {
-    return D <= 64 ? attn::prompt_t<QT, 64>() : D <= 128 ? attn::prompt_t<QT, 128>() : attn::prompt_t<QT, 256>();
 }
 template <typename QT, typename KT> hipError_t launch_prompt(const AttnParams& p, hipStream_t st) {
     if (p.D <= 64) return attn::prompt_dp<QT, KT, 64>(p, st);

@@ -39,13 +39,17 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 __device__ __forceinline__ float clamp448(float x) { return x != x ? x : fminf(fmaxf(x, -448.0f), 448.0f); }
 
-// One lane: eight elements of one token's key or value (blockIdx.y).
+// Eight elements of one token's key or value, in flight and then stored.
+template <typename QT> struct Chunk { u32x4_t w[sizeof(QT) / 2]; };
+
+// `lanes` lanes (a power of two) a token, each every lanes-th chunk of its key
+// and its value, two of each in flight.
 template <typename QT, bool E4M3>
-__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams p, int shift) {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int tok = (int)(id / p.chunks), ch = (int)(id - (int64_t)tok * p.chunks);
-    if (tok >= p.tokens) return;
-    int row = tok, pos;
+    if (id >> shift >= p.tokens) return;
+    const int tok = (int)(id >> shift), lanes = 1 << shift;
+    int row = tok, pos = 1;
     if (p.off) {
         // the row whose run holds the token: the last one that begins at or before it
         int a = 0, b = p.rows;  // off[a] <= tok, off[b] > tok
@@ -57,35 +61,51 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
         }
         row = a;
         pos = p.off[row + 1] - tok;
-    } else {
-        pos = 1;
     }
+    const QT* k = static_cast<const QT*>(p.k) + (int64_t)tok * p.ks;
+    const QT* v = static_cast<const QT*>(p.v) + (int64_t)tok * p.vs;
     pos = min(max(p.len[row], 0), p.maxb * p.ps) - pos;
     if (pos < 0) return;
     const int blk = pos / p.ps, pg = p.table[(int64_t)row * p.maxb + blk];
     if (pg < 0 || pg >= p.np) return;
-    const int e = ch * 8, h = e / p.D, d = e - h * p.D;
-    const bool val = blockIdx.y != 0;
-    const QT* src = static_cast<const QT*>(val ? p.v : p.k) + (int64_t)tok * (val ? p.vs : p.ks) + e;
-    const int64_t at = (int64_t)pg * (val ? p.vps : p.kps) + ((int64_t)h * p.ps + (pos - blk * p.ps)) * p.D + d;
-    void* dst = val ? p.vc : p.kc;
-    if constexpr (E4M3) {
-        float x[8];
-        Io<QT, 8>::load(src, x);
-        const float s = (val ? p.vscale : p.kscale)[h];
+    const int in = pos - blk * p.ps;
+    auto put = [&](void* cache, int64_t page, const float* scale, int h, int d, const Chunk<QT>& x) {
+        const int64_t at = page + ((int64_t)h * p.ps + in) * p.D + d;
+        if constexpr (E4M3) {
+            float y[8];
+            Io<QT, 8>::unpack(x.w[0], y);
+            const float s = scale[h];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = clamp448(x[i] / s);
-        typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-        u32x2_t w = {e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7])};
+            for (int i = 0; i < 8; ++i) y[i] = clamp448(y[i] / s);
+            typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+            u32x2_t w = {e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7])};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)  // one code for NaN: the conversion gives 0xff
-            if (x[i] != x[i]) w[i >> 2] &= ~(0x80u << (i & 3) * 8);
-        *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(dst) + at) = w;
-    } else {
-        constexpr int N = 8 * sizeof(QT) / 16;
+            for (int i = 0; i < 8; ++i)  // one code for NaN: the conversion gives 0xff
+                if (y[i] != y[i]) w[i >> 2] &= ~(0x80u << (i & 3) * 8);
+            *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(cache) + at) = w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            reinterpret_cast<u32x4_t*>(static_cast<QT*>(dst) + at)[i] = reinterpret_cast<const u32x4_t*>(src)[i];
+            for (int i = 0; i < (int)sizeof(QT) / 2; ++i) reinterpret_cast<u32x4_t*>(static_cast<QT*>(cache) + at)[i] = x.w[i];
+        }
+    };
+    for (int c0 = (int)id & (lanes - 1); c0 < p.chunks; c0 += 2 * lanes) {
+        Chunk<QT> x[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int c = c0 + u * lanes;
+            if (c < p.chunks) {
+                x[u][0] = *reinterpret_cast<const Chunk<QT>*>(k + c * 8);
+                x[u][1] = *reinterpret_cast<const Chunk<QT>*>(v + c * 8);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int c = c0 + u * lanes, h = c * 8 / p.D, d = c * 8 - h * p.D;
+            if (c < p.chunks) {
+                put(p.kc, (int64_t)pg * p.kps, p.kscale, h, d, x[u][0]);
+                put(p.vc, (int64_t)pg * p.vps, p.vscale, h, d, x[u][1]);
+            }
+        }
     }
 }
 
@@ -115,23 +135,37 @@ template <typename I> __device__ __forceinline__ I scan_excl(I x, I* ws, I& tota
     return before + s - x;
 }
 
+constexpr int kRefs = 16;  // counts that a lane looks at in one go
+
+// Bit j: page i + j is live, or not a page.
+__device__ __forceinline__ uint32_t live_pages(const int32_t* refs, int np, int i) {
+    typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
+    uint32_t live = 0u;
+    if (i + kRefs <= np && (reinterpret_cast<uintptr_t>(refs) & 15u) == 0) {
+        i32x4_t r[kRefs / 4];
+#pragma unroll
+        for (int j = 0; j < kRefs / 4; ++j) r[j] = reinterpret_cast<const i32x4_t*>(refs + i)[j];
+#pragma unroll
+        for (int j = 0; j < kRefs; ++j) live |= (uint32_t)(r[j >> 2][j & 3] > 0) << j;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kRefs; ++j) live |= (uint32_t)(i + j >= np || refs[i + j] > 0) << j;
+    }
+    return live;
+}
+
 // The lowest `want` free pages, ascending, into `fresh`; the count of free
 // pages if it is below `want`, else any number >= want.
 __device__ int find_free(const int32_t* refs, int np, int want, int32_t* fresh, int* ws) {
     int found = 0;
-    for (int base = 0; base < np && found < want; base += NT * 4) {
-        const int i = base + threadIdx.x * 4;
-        int r[4], n = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            r[j] = i + j < np ? refs[i + j] : 1;
-            n += r[j] <= 0;
-        }
+    for (int base = 0; base < np && found < want; base += NT * kRefs) {
+        const int i = base + threadIdx.x * kRefs;
+        const uint32_t live = live_pages(refs, np, i);
         int total;
-        int at = found + scan_excl(n, ws, total);
+        int at = found + scan_excl((int)__popc(~live & (kRefs >= 32 ? ~0u : (1u << kRefs) - 1u)), ws, total);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (r[j] <= 0) {
+        for (int j = 0; j < kRefs; ++j)
+            if (!(live >> j & 1u)) {
                 if (at < want) fresh[at] = i + j;
                 ++at;
             }
@@ -318,6 +352,7 @@ __global__ void __launch_bounds__(256) free_kernel(const CacheParams p, const in
     const int row = rows[blockIdx.y];
     if (row < 0 || row >= p.rows) return;
     const int b = blockIdx.x * 256 + threadIdx.x;
+    if (window == 0 && b == 0) p.len[row] = 0;
     if (b >= p.maxb) return;
     if (window > 0) {
         const int len = row_len(p, row), lo = len - window + 1;  // the tokens from lo on stay
@@ -329,47 +364,39 @@ __global__ void __launch_bounds__(256) free_kernel(const CacheParams p, const in
     const int pg = atomicExch(e, -1);
     if (pg >= 0 && pg < p.np) atomicSub(&p.refs[pg], 1);
 }
-__global__ void __launch_bounds__(256) clear_len_kernel(const CacheParams p, int n, const int32_t* rows) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i < n && rows[i] >= 0 && rows[i] < p.rows) p.len[rows[i]] = 0;
-}
-
 // ---------------------------------------------------------------- compact
 
 // The moves: fresh[p] = new place of page p; pair[2k], pair[2k + 1] = from, to
 // of move k; owner[0] = their count (rows >= 1) -- kept in pair's last word.
 __global__ void __launch_bounds__(NT) compact_plan_kernel(const CacheParams p, int32_t* refs_out, int32_t* moved) {
     __shared__ int ws[NT / 64];
+    __shared__ int64_t ws64[NT / 64];
+    constexpr uint32_t kMask = (1u << kRefs) - 1u;
+    // bits of the pages of a lane's range that exist, and that lie below n
+    auto below = [](int i, int n) { return n <= i ? 0u : n - i >= kRefs ? kMask : (1u << (n - i)) - 1u; };
     int live = 0;
-    for (int base = 0; base < p.np; base += NT * 4) {
-        const int i = base + threadIdx.x * 4;
-        int n = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) n += i + j < p.np && p.refs[i + j] > 0;
+    for (int base = 0; base < p.np; base += NT * kRefs) {
+        const int i = base + threadIdx.x * kRefs;
         int total;
-        scan_excl(n, ws, total);
+        scan_excl((int)__popc(live_pages(p.refs, p.np, i) & below(i, p.np)), ws, total);
         live += total;
     }
     int holes = 0, movers = 0;
-    for (int base = 0; base < p.np; base += NT * 4) {
-        const int i = base + threadIdx.x * 4;
-        int r[4], nh = 0, nm = 0;
+    for (int base = 0; base < p.np; base += NT * kRefs) {
+        const int i = base + threadIdx.x * kRefs;
+        const uint32_t l = live_pages(p.refs, p.np, i), hole = ~l & below(i, live), mover = l & below(i, p.np) & ~below(i, live);
+        // both sums in one scan
+        int64_t total;
+        const int64_t before = scan_excl((int64_t)__popc(hole) << 32 | (int64_t)__popc(mover), ws64, total);
+        int ah = holes + (int)(before >> 32), am = movers + (int)(uint32_t)before;
+        holes += (int)(total >> 32);
+        movers += (int)(uint32_t)total;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            r[j] = i + j < p.np ? p.refs[i + j] : 0;
-            nh += i + j < live && r[j] <= 0;
-            nm += i + j >= live && r[j] > 0;
-        }
-        int th, tm;
-        int ah = holes + scan_excl(nh, ws, th), am = movers + scan_excl(nm, ws, tm);
-        holes += th;
-        movers += tm;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kRefs; ++j) {
             if (i + j >= p.np) continue;
             p.fresh[i + j] = i + j;
-            if (i + j < live && r[j] <= 0) p.pair[2 * ah++ + 1] = i + j;
-            if (i + j >= live && r[j] > 0) p.pair[2 * am++] = i + j;
+            if (hole >> j & 1u) p.pair[2 * ah++ + 1] = i + j;
+            if (mover >> j & 1u) p.pair[2 * am++] = i + j;
         }
     }
     __syncthreads();
@@ -506,13 +533,14 @@ extern "C" int cache_append(const bcg_append_args* a, void* stream) {
     p.ks = a->k_stride; p.vs = a->v_stride; p.kps = a->k_page_stride; p.vps = a->v_page_stride;
     p.rows = a->rows; p.tokens = a->tokens; p.kvh = a->kv_heads; p.D = a->head_dim;
     p.ps = a->page_size; p.maxb = a->max_blocks; p.np = a->num_pages; p.chunks = (int)(width / 8);
-    const int64_t blocks = ((int64_t)a->tokens * p.chunks + 255) / 256;
-    if (blocks > INT32_MAX) return fail(BCG_ESHAPE, "%s: too many tokens", who);
-    const dim3 grid((unsigned)blocks, 2);
+    int shift = 0;
+    while (shift < 6 && (1 << shift) < p.chunks) ++shift;
+    const int64_t blocks = (((int64_t)a->tokens << shift) + 255) / 256;
+    const dim3 grid((unsigned)blocks);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (a->kv_dtype == BCG_E4M3) hipLaunchKernelGGL((append_kernel<bf16_t, true>), grid, dim3(256), 0, st, p);
-    else if (a->dtype == BCG_BF16) hipLaunchKernelGGL((append_kernel<bf16_t, false>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((append_kernel<float, false>), grid, dim3(256), 0, st, p);
+    if (a->kv_dtype == BCG_E4M3) hipLaunchKernelGGL((append_kernel<bf16_t, true>), grid, dim3(256), 0, st, p, shift);
+    else if (a->dtype == BCG_BF16) hipLaunchKernelGGL((append_kernel<bf16_t, false>), grid, dim3(256), 0, st, p, shift);
+    else hipLaunchKernelGGL((append_kernel<float, false>), grid, dim3(256), 0, st, p, shift);
     return hip_status(hipGetLastError(), "cache_append: launch");
 }
 
@@ -554,15 +582,8 @@ extern "C" int cache_free(const bcg_cache* c, int n, const int32_t* rows, int wi
     if (n > 65535) return fail(BCG_ESHAPE, "cache_free: a list of %d entries (at most 65535)", n);
     if (!rows) return fail(BCG_EINVAL, "cache_free: NULL list");
     hipStream_t st = static_cast<hipStream_t>(stream);
-    hipError_t e = hipSuccess;
-    if (p.maxb > 0) {
-        hipLaunchKernelGGL(free_kernel, dim3((unsigned)((p.maxb + 255) / 256), n), dim3(256), 0, st, p, rows, window, sinks);
-        e = hipGetLastError();
-    }
-    if (e == hipSuccess && window == 0) {
-        hipLaunchKernelGGL(clear_len_kernel, dim3((n + 255) / 256), dim3(256), 0, st, p, n, rows);
-        e = hipGetLastError();
-    }
+    hipLaunchKernelGGL(free_kernel, dim3((unsigned)((p.maxb + 255) / 256 + (p.maxb == 0)), n), dim3(256), 0, st, p, rows, window, sinks);
+    const hipError_t e = hipGetLastError();
     return hip_status(e, "cache_free: launch");
 }
 

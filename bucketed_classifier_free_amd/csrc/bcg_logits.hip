@@ -4,9 +4,11 @@
 // HBM-bound: per token it reads c and u, writes z, and does a few fp32
 // operations.  A workgroup takes kSeg consecutive tokens of one sample.  The
 // sparse inputs (the history's tokens, the biased ids) become dense in LDS
-// first: the workgroup runs over the sample's lists and counts those that
-// fall into its tokens, while its logits are on their way.  Integer counts
-// and the largest index win by LDS atomics, so no order changes a result.
+// first, one word a token: the workgroup runs over the sample's lists and
+// enters those that fall into its tokens, while its logits are on their way.
+// Counts add up and the largest bias index wins by LDS atomics, so no order
+// changes a result.  Most vectors of eight tokens have nothing entered, which
+// one test of their words tells.
 #include "bcg_device.h"
 #include "bcg_launch.h"
 #include "bcg_decode.h"
@@ -18,6 +20,11 @@ constexpr int NT = 256;
 constexpr int kVec = 8;                 // tokens of one lane's vector
 constexpr int kRounds = 2;              // vectors of a lane
 constexpr int kSeg = NT * kVec * kRounds;
+
+// The word of a token: 1 + the last bias of the token (low 13 bits), its
+// times in the answer (18 bits), whether the prompt holds it (the top bit).
+constexpr uint32_t kBiasMask = 0x1fffu, kOnce = 0x2000u, kPrompt = 0x80000000u;
+static_assert(BCG_MAX_BIASES + 1 <= (int)kBiasMask + 1 && BCG_MAX_HISTORY * (uint64_t)kOnce < kPrompt, "");
 
 struct LogitsParams {
     int n, vocab, rows, hist, biases, words;
@@ -86,8 +93,7 @@ template <typename T> __device__ __forceinline__ void store8(T* p, int left, con
 
 template <typename T, typename OT, bool SPARSE>
 __global__ void __launch_bounds__(NT) logits_kernel(const LogitsParams p) {
-    __shared__ uint32_t cnt[SPARSE ? kSeg : 1];   // 0: not in the history; low 31 bits: times in the answer
-    __shared__ uint32_t last[SPARSE ? kSeg : 1];  // 1 + the last bias of the token, 0: none
+    __shared__ __attribute__((aligned(16))) uint32_t word[SPARSE ? kSeg : 4];
     const int i = blockIdx.y, s0 = blockIdx.x * kSeg, tid = threadIdx.x;
     const int cr = p.cond[i];
     if (cr < 0 || cr >= p.rows) return;
@@ -106,30 +112,45 @@ __global__ void __launch_bounds__(NT) logits_kernel(const LogitsParams p) {
         if (guided) load8<T>(urow + j, p.vocab - j, u[r]);
     }
     if constexpr (SPARSE) {
-        for (int k = tid; k < kSeg; k += NT) cnt[k] = last[k] = 0u;
+        const int hl = p.history ? min(max(p.hlen[i], 0), p.hist) : 0, pl = p.plen ? p.plen[i] : 0;
+        const int32_t* h = p.history + (int64_t)i * p.hist;
+        constexpr int U = 8;  // entries of a lane on their way
+        int e[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) e[k] = k * NT + tid < hl ? h[k * NT + tid] : -1;
+#pragma unroll
+        for (int k = 0; k < kSeg / NT / 4; ++k) reinterpret_cast<u32x4_t*>(word)[k * NT + tid] = u32x4_t{0, 0, 0, 0};
         __syncthreads();
-        if (p.history) {
-            const int hl = min(max(p.hlen[i], 0), p.hist), pl = p.plen ? p.plen[i] : 0;
-            const int32_t* h = p.history + (int64_t)i * p.hist;
-            for (int k = tid; k < hl; k += NT) {
-                const unsigned at = (unsigned)(h[k] - s0);
-                if (at < (unsigned)kSeg) {
-                    if (k >= pl) atomicAdd(&cnt[at], 1u);
-                    else atomicOr(&cnt[at], 0x80000000u);
+        for (int k0 = 0; k0 < hl; k0 += U * NT) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const unsigned at = (unsigned)(e[k] - s0);
+                // e = -1 (none) is below every segment; ids below 0 or beyond the vocabulary meet no stored token
+                if (e[k] >= s0 && at < (unsigned)kSeg) {
+                    if (k0 + k * NT + tid >= pl) atomicAdd(&word[at], kOnce);
+                    else atomicOr(&word[at], kPrompt);
                 }
+                const int next = k0 + (U + k) * NT + tid;
+                e[k] = next < hl ? h[next] : -1;
             }
         }
         if (p.bias_ids) {
             const int32_t* b = p.bias_ids + (int64_t)i * p.biases;
             for (int k = tid; k < p.biases; k += NT) {
-                const unsigned at = (unsigned)(b[k] - s0);
-                if (at < (unsigned)kSeg) atomicMax(&last[at], (unsigned)k + 1u);
+                const int id = b[k];
+                if (id < s0 || id - s0 >= kSeg) continue;
+                uint32_t old = word[id - s0];
+                while ((old & kBiasMask) < (uint32_t)k + 1u) {
+                    const uint32_t seen = atomicCAS(&word[id - s0], old, (old & ~kBiasMask) | ((uint32_t)k + 1u));
+                    if (seen == old) break;
+                    old = seen;
+                }
             }
         }
         __syncthreads();
     }
     const float rep = p.rep ? p.rep[i] : 1.0f, pres = p.pres ? p.pres[i] : 0.0f, freq = p.freq ? p.freq[i] : 0.0f;
-    const float temp = p.temp ? p.temp[i] : 1.0f;
+    const float cool = p.temp ? 1.0f / p.temp[i] : 1.0f;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
         const int j = s0 + (r * NT + tid) * kVec, left = p.vocab - j;
@@ -138,22 +159,23 @@ __global__ void __launch_bounds__(NT) logits_kernel(const LogitsParams p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] = guided && u[r][e] != c[r][e] ? __builtin_fmaf(w, c[r][e] - u[r][e], u[r][e]) : c[r][e];
         if constexpr (SPARSE) {
+            const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(&word[j - s0]), hi = *reinterpret_cast<const u32x4_t*>(&word[j - s0 + 4]);
+            if ((lo[0] | lo[1]) | (lo[2] | lo[3]) | (hi[0] | hi[1]) | (hi[2] | hi[3])) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t n = cnt[j - s0 + e], b = last[j - s0 + e];
-                if (n) {
-                    z[e] = z[e] > 0.0f ? z[e] / rep : z[e] * rep;
-                    const uint32_t m = n & 0x7fffffffu;
-                    z[e] = z[e] - freq * (float)m;
-                    if (m) z[e] = z[e] - pres;
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t n = e < 4 ? lo[e & 3] : hi[e & 3];
+                    if (n & ~kBiasMask) {
+                        z[e] = z[e] > 0.0f ? z[e] / rep : z[e] * rep;
+                        const uint32_t m = (n & ~kPrompt) / kOnce;
+                        z[e] = z[e] - freq * (float)m;
+                        if (m) z[e] = z[e] - pres;
+                    }
+                    if (n & kBiasMask) z[e] = z[e] + p.bias[(int64_t)i * p.biases + (n & kBiasMask) - 1];
                 }
-                if (b) z[e] = z[e] + p.bias[(int64_t)i * p.biases + b - 1];
             }
         }
-        if (temp != 1.0f) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = z[e] / temp;
-        }
+        for (int e = 0; e < 8; ++e) z[e] = z[e] * cool;
         if (p.mask) {
             const uint32_t bits = p.mask[(int64_t)i * p.words * 4 + (j >> 3)];
 #pragma unroll
@@ -192,6 +214,8 @@ extern "C" int guided_logits(const bcg_logits_args* a, void* stream) {
     const bool penal = a->repetition || a->presence || a->frequency || a->prompt_len || a->history_len;
     if (!a->history && penal) return fail(BCG_EINVAL, "%s: penalties without a history", who);
     if (a->history && (!a->history_len || a->max_history < 0)) return fail(BCG_EINVAL, "%s: a history without its lengths", who);
+    if (a->history && a->max_history > BCG_MAX_HISTORY)
+        return fail(BCG_ESHAPE, "%s: a history of %d tokens (at most %d)", who, a->max_history, BCG_MAX_HISTORY);
     if ((a->bias_ids == nullptr) != (a->bias == nullptr)) return fail(BCG_EINVAL, "%s: bias and bias_ids go together", who);
     if (a->bias_ids && (a->num_biases < 0 || a->num_biases > BCG_MAX_BIASES))
         return fail(BCG_ESHAPE, "%s: %d biases not in [0, %d]", who, a->num_biases, BCG_MAX_BIASES);

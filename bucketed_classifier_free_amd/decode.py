@@ -88,7 +88,7 @@ def attention_workspace(tokens: int, q_heads: int, head_dim: int, device=None):
     """A workspace for the attention calls of up to ``tokens`` query rows
     (keep it from call to call; one for each stream)."""
     n = L.lib().attention_workspace_size(int(tokens), int(q_heads), int(head_dim))
-    return torch.zeros(n, dtype=torch.uint8, device=device or torch.device("cuda", torch.cuda.current_device()))
+    return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda", torch.cuda.current_device()))
 
 
 def _attention(prompt, q, q_offset, k_cache, v_cache, block_table, kv_len, out, *, workspace, scale, window, sinks,

@@ -42,6 +42,7 @@ enum { BCG_E4M3 = 2 };               /* storage type of a cache, next to BCG_F32
 #define BCG_MAX_HEAD_DIM 256
 #define BCG_MAX_PAGE_SIZE 1024
 #define BCG_MAX_BIASES 4096          /* biases a row in guided_logits */
+#define BCG_MAX_HISTORY 262143       /* tokens a row of its history */
 
 /*
  * paged_attention -- one new token a row over its pages.  For query head h of
@@ -68,8 +69,8 @@ enum { BCG_E4M3 = 2 };               /* storage type of a cache, next to BCG_F32
  * A hidden token's storage takes no part, as above.
  *
  * workspace: attention_workspace_size(tokens, q_heads, head_dim) bytes,
- * 16-byte aligned, zero before its first use; every call leaves what the next
- * one needs.  Calls that may run at the same time need workspaces of their own.
+ * 16-byte aligned, any contents.  Calls that may run at the same time need
+ * workspaces of their own.
  * max_len and max_new are upper bounds of kv_len and of a row's new tokens
  * (they size the launch: tokens beyond them are not seen, queries beyond them
  * not computed).
@@ -212,7 +213,7 @@ int cache_copy(const bcg_cache* cache, int n, const int32_t* src, const int32_t*
  *   repetition (j in history[i]):  z = z > 0 ? z / rep[i] : z * rep[i]
  *   frequency, presence:           z = z - freq[i] * m - (m > 0 ? pres[i] : 0)
  *   bias:                          z = z + bias[i, b], bias_ids[i, b] == j (the last such b)
- *   temperature:                   z = z / temperature[i]
+ *   temperature:                   z = z * (1 / temperature[i])
  *   grammar mask:                  z = -infinity where bit j of mask[i] is 0
  * with c = logits[cond_row[i], j], u = logits[uncond_row[i], j] and m the count
  * of j among the answer's tokens history[i, prompt_len[i] .. history_len[i])
