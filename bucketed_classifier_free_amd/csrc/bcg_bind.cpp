@@ -1,0 +1,402 @@
+// The argument checks and marshalling of decode.py's calls, as a CPython
+// module (_bind): a decoding step makes a handful of these calls for every
+// layer, and the smallest kernels behind them run for a few microseconds,
+// less than Python takes to look at the dozen tensors of a call.
+//
+// The functions take what decode.py's wrappers pass, positionally, check it
+// (ValueError before any call), and return the library's status code.  The
+// library's entry points come in through setup(), so that loading it stays
+// with _lib.py.
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <c10/core/DeviceGuard.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <initializer_list>
+#include <optional>
+#include <string>
+
+#include "bcg_decode.h"
+
+namespace {
+
+struct Refused {};
+
+[[noreturn]] void refuse(const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    PyErr_FormatV(PyExc_ValueError, fmt, ap);
+    va_end(ap);
+    throw Refused{};
+}
+
+enum { ATTN_PAGED, ATTN_PROMPT, APPEND, EXTEND, FORK, FREE, COMPACT, COPY, LOGITS, WORKSPACE, ENTRIES };
+void* g_entry[ENTRIES];
+PyObject* g_raw_stream;
+
+template <typename F> F entry(int i) { return reinterpret_cast<F>(g_entry[i]); }
+
+const at::Tensor& tensor(PyObject* o, const char* name) {
+    if (!THPVariable_Check(o)) refuse("%s: expected a torch tensor", name);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda()) refuse("%s: must be a GPU tensor (got %s)", name, t.device().str().c_str());
+    return t;
+}
+
+// The arguments of one call: checks each tensor, all on one device.
+struct Call {
+    int device = -1;
+    std::optional<c10::DeviceGuard> guard;
+
+    const at::Tensor& on_device(PyObject* o, const char* name) {
+        const at::Tensor& t = tensor(o, name);
+        if (device < 0) {
+            device = t.get_device();
+            guard.emplace(t.device());
+        } else if (t.get_device() != device) {
+            refuse("%s: on another GPU than the call's first tensor", name);
+        }
+        return t;
+    }
+    // A contiguous tensor of this type and shape (-1: any extent).
+    const at::Tensor& whole(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) {
+        const at::Tensor& t = on_device(o, name);
+        if (t.scalar_type() != type) refuse("%s: dtype %s, expected %s", name, c10::toString(t.scalar_type()), c10::toString(type));
+        if (!t.is_contiguous()) refuse("%s: must be contiguous", name);
+        bool same = t.dim() == (int64_t)shape.size();
+        int64_t d = 0;
+        for (int64_t n : shape) {
+            if (same && n >= 0 && t.size(d) != n) same = false;
+            ++d;
+        }
+        if (!same) {
+            std::string want;
+            for (int64_t n : shape) want += (want.empty() ? "" : ", ") + (n < 0 ? std::string("any") : std::to_string(n));
+            std::string got;
+            for (int64_t n : t.sizes()) got += (got.empty() ? "" : ", ") + std::to_string(n);
+            refuse("%s: shape [%s], expected [%s]", name, got.c_str(), want.c_str());
+        }
+        return t;
+    }
+    template <typename T> T* ptr(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) {
+        return static_cast<T*>(whole(o, name, type, shape).data_ptr());
+    }
+    template <typename T> T* opt(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) {
+        return o == Py_None ? nullptr : ptr<T>(o, name, type, shape);
+    }
+    // A tensor whose dimensions after the first are contiguous; its row stride.
+    const at::Tensor& rows(PyObject* o, const char* name, int dims, int64_t& stride) {
+        const at::Tensor& t = on_device(o, name);
+        if (t.dim() != dims) refuse("%s: expected %d dimensions, got %d", name, dims, (int)t.dim());
+        int64_t width = 1;
+        for (int d = dims - 1; d > 0; --d) {
+            if (t.size(d) != 1 && t.stride(d) != width) refuse("%s: must be contiguous after its first dimension", name);
+            width *= t.size(d);
+        }
+        stride = t.size(0) > 1 || t.stride(0) > width ? t.stride(0) : width;
+        return t;
+    }
+    void* stream(PyObject* given) const {
+        PyObject* s;
+        if (given == Py_None) {
+            PyObject* d = PyLong_FromLong(device);
+            if (!d) throw Refused{};
+            s = PyObject_CallOneArg(g_raw_stream, d);
+            Py_DECREF(d);
+        } else {
+            s = PyObject_GetAttrString(given, "cuda_stream");
+        }
+        if (!s) throw Refused{};
+        void* p = PyLong_AsVoidPtr(s);
+        Py_DECREF(s);
+        if (!p && PyErr_Occurred()) throw Refused{};
+        return p;
+    }
+};
+
+int32_t i32(int64_t x, const char* name) {
+    if (x < INT32_MIN || x > INT32_MAX) refuse("%s: %lld is out of range", name, (long long)x);
+    return (int32_t)x;
+}
+int32_t integer(PyObject* o, const char* name) {
+    const long long x = PyLong_AsLongLong(o);
+    if (x == -1 && PyErr_Occurred()) throw Refused{};
+    return i32(x, name);
+}
+
+constexpr at::ScalarType F32 = at::kFloat, BF16 = at::kBFloat16, E4M3 = at::kFloat8_e4m3fn, I32 = at::kInt, U8 = at::kByte;
+
+int32_t storage(const at::Tensor& t, const char* name) {
+    if (t.scalar_type() == F32) return BCG_F32;
+    if (t.scalar_type() == BF16) return BCG_BF16;
+    refuse("%s must be float32 or bfloat16", name);
+}
+
+// One layer's pages and the rows' tables: o = k_cache, v_cache, block_table,
+// kv_len, k_scale, v_scale; fills the members that bcg_attn_args and
+// bcg_append_args share.
+template <typename A> void cache_args(Call& c, A& a, PyObject* const* o, at::ScalarType type, const void*& k, const void*& v) {
+    const at::Tensor& kt = c.rows(o[0], "k_cache", 4, a.k_page_stride);
+    const at::Tensor& vt = c.rows(o[1], "v_cache", 4, a.v_page_stride);
+    if (kt.scalar_type() != vt.scalar_type() || kt.sizes() != vt.sizes()) refuse("k_cache and v_cache must have the same shape and dtype");
+    const at::ScalarType ct = kt.scalar_type();
+    if (ct != type && !(ct == E4M3 && type == BF16)) refuse("a cache of %s does not go with %s", c10::toString(ct), c10::toString(type));
+    a.kv_dtype = ct == E4M3 ? (int)BCG_E4M3 : ct == BF16 ? (int)BCG_BF16 : (int)BCG_F32;
+    a.num_pages = i32(kt.size(0), "k_cache");
+    a.kv_heads = i32(kt.size(1), "k_cache");
+    a.page_size = i32(kt.size(2), "k_cache");
+    const at::Tensor& t = c.whole(o[2], "block_table", I32, {-1, -1});
+    a.rows = i32(t.size(0), "block_table");
+    a.max_blocks = i32(t.size(1), "block_table");
+    a.block_table = static_cast<const int32_t*>(t.data_ptr());
+    a.kv_len = c.ptr<const int32_t>(o[3], "kv_len", I32, {a.rows});
+    a.k_scale = c.opt<const float>(o[4], "k_scale", F32, {a.kv_heads});
+    a.v_scale = c.opt<const float>(o[5], "v_scale", F32, {a.kv_heads});
+    k = kt.data_ptr();
+    v = vt.data_ptr();
+}
+
+// Runs `f`, turning refusals and other exceptions into Python's.
+template <typename F> PyObject* guarded(F f) {
+    try {
+        return PyLong_FromLong(f());
+    } catch (const Refused&) {
+        return nullptr;
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+#define NEED(n) \
+    if (nargs != (n)) { PyErr_SetString(PyExc_TypeError, "wrong number of arguments"); return nullptr; }
+
+// prompt, q, q_offset, k_cache, v_cache, block_table, kv_len, k_scale, v_scale, out, lse, workspace, scale, window,
+// sinks, max_len, max_new, stream
+PyObject* attention(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+    NEED(18);
+    return guarded([&] {
+        Call c;
+        bcg_attn_args a{};
+        const bool prompt = o[0] == Py_True;
+        const at::Tensor& q = c.rows(o[1], "q", 3, a.q_stride);
+        a.q_dtype = storage(q, "q");
+        a.q = q.data_ptr();
+        a.tokens = i32(q.size(0), "q");
+        a.q_heads = i32(q.size(1), "q");
+        a.head_dim = i32(q.size(2), "q");
+        cache_args(c, a, o + 3, q.scalar_type(), a.k_cache, a.v_cache);
+        const int64_t dim = THPVariable_Unpack(o[3]).size(3);
+        if (dim != a.head_dim) refuse("head_dim %d of q, %d of the cache", a.head_dim, (int)dim);
+        if (prompt) a.q_offset = c.ptr<const int32_t>(o[2], "q_offset", I32, {(int64_t)a.rows + 1});
+        else if (a.rows != a.tokens) refuse("%d query rows for %d rows of the table", a.tokens, a.rows);
+        a.out = c.ptr<void>(o[9], "out", q.scalar_type(), {a.tokens, a.q_heads, a.head_dim});
+        a.lse = c.opt<float>(o[10], "lse", F32, {a.tokens, a.q_heads});
+        const at::Tensor& w = c.whole(o[11], "workspace", U8, {-1});
+        a.workspace = w.data_ptr();
+        a.workspace_bytes = (size_t)w.numel();
+        const double scale = o[12] == Py_None ? 1.0 / std::sqrt((double)a.head_dim) : PyFloat_AsDouble(o[12]);
+        if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
+        a.scale = (float)scale;
+        a.window = integer(o[13], "window");
+        a.sinks = integer(o[14], "sinks");
+        a.max_len = o[15] == Py_None ? i32((int64_t)a.max_blocks * a.page_size, "max_len") : integer(o[15], "max_len");
+        a.max_new = o[16] == Py_None ? a.tokens : integer(o[16], "max_new");
+        return entry<int (*)(const bcg_attn_args*, void*)>(prompt ? ATTN_PROMPT : ATTN_PAGED)(&a, c.stream(o[17]));
+    });
+}
+
+// k, v, offset, k_cache, v_cache, block_table, kv_len, k_scale, v_scale, stream
+PyObject* append(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+    NEED(10);
+    return guarded([&] {
+        Call c;
+        bcg_append_args a{};
+        const at::Tensor& k = c.rows(o[0], "k", 3, a.k_stride);
+        const at::Tensor& v = c.rows(o[1], "v", 3, a.v_stride);
+        if (k.scalar_type() != v.scalar_type() || k.sizes() != v.sizes()) refuse("k and v must have the same shape and dtype");
+        a.dtype = storage(k, "k and v");
+        a.k = k.data_ptr();
+        a.v = v.data_ptr();
+        a.tokens = i32(k.size(0), "k");
+        const void *kc, *vc;
+        cache_args(c, a, o + 3, k.scalar_type(), kc, vc);
+        a.k_cache = const_cast<void*>(kc);
+        a.v_cache = const_cast<void*>(vc);
+        a.head_dim = i32(THPVariable_Unpack(o[3]).size(3), "k_cache");
+        if (k.size(1) != a.kv_heads || k.size(2) != a.head_dim) refuse("k and v must be [tokens, %d, %d]", a.kv_heads, a.head_dim);
+        a.offset = c.opt<const int32_t>(o[2], "offset", I32, {(int64_t)a.rows + 1});
+        if (!a.offset && a.rows != a.tokens) refuse("%d tokens for %d rows of the table", a.tokens, a.rows);
+        return entry<int (*)(const bcg_append_args*, void*)>(APPEND)(&a, c.stream(o[9]));
+    });
+}
+
+// pool, table, length, refs -> bcg_cache; false for the workspace if `work` is None or too small for n
+void pool_args(Call& c, bcg_cache& a, PyObject* o) {
+    const at::Tensor& p = c.on_device(o, "pool");
+    if (p.dim() != 5) refuse("pool must be [planes, num_pages, kv_heads, page_size, head_dim]");
+    const int64_t heads = p.size(2), page = p.size(3), dim = p.size(4), width = heads * page * dim;
+    if ((p.stride(4) != 1 && dim != 1) || (p.stride(3) != dim && page != 1) || (p.stride(2) != page * dim && heads != 1))
+        refuse("pool: a page must be contiguous");
+    const int64_t e = (int64_t)p.element_size();
+    a.planes = i32(p.size(0), "pool");
+    a.num_pages = i32(p.size(1), "pool");
+    a.page_size = i32(page, "pool");
+    a.plane_stride = p.stride(0) * e;
+    a.page_stride = (a.num_pages > 1 ? p.stride(1) : width) * e;
+    a.page_bytes = width * e;
+    a.pool = p.data_ptr();
+}
+bool tables_args(Call& c, bcg_cache& a, PyObject* const* o, int n) {
+    pool_args(c, a, o[0]);
+    const at::Tensor& t = c.whole(o[1], "table", I32, {-1, -1});
+    a.rows = i32(t.size(0), "table");
+    a.max_blocks = i32(t.size(1), "table");
+    a.block_table = static_cast<int32_t*>(t.data_ptr());
+    a.kv_len = c.ptr<int32_t>(o[2], "length", I32, {a.rows});
+    a.refs = c.ptr<int32_t>(o[3], "refs", I32, {a.num_pages});
+    if (o[4] == Py_None) return false;
+    const at::Tensor& w = c.whole(o[4], "workspace", U8, {-1});
+    a.workspace = w.data_ptr();
+    a.workspace_bytes = (size_t)w.numel();
+    return a.workspace_bytes >= entry<size_t (*)(int, int, int)>(WORKSPACE)(a.rows, a.num_pages, n);
+}
+constexpr int kNoWorkspace = 1;  // to decode.py: make a workspace and call again
+
+// The list operators: pool, table, length, refs, workspace, then the lists, ..., stream
+int32_t* list(Call& c, PyObject* o, const char* name, int64_t n) { return c.ptr<int32_t>(o, name, I32, {n}); }
+int entries(Call& c, PyObject* o, const char* name) { return i32(c.whole(o, name, I32, {-1}).size(0), name); }
+
+// ..., rows, count, granted, stream
+PyObject* extend(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+    NEED(9);
+    return guarded([&] {
+        Call c;
+        bcg_cache a{};
+        const int n = entries(c, o[5], "rows");
+        if (!tables_args(c, a, o, n)) return kNoWorkspace;
+        return entry<int (*)(const bcg_cache*, int, const int32_t*, const int32_t*, int32_t*, void*)>(EXTEND)(
+            &a, n, list(c, o[5], "rows", n), list(c, o[6], "count", n), list(c, o[7], "granted", n), c.stream(o[8]));
+    });
+}
+// ..., src, dst, granted, stream
+PyObject* fork(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+    NEED(9);
+    return guarded([&] {
+        Call c;
+        bcg_cache a{};
+        const int n = entries(c, o[5], "src");
+        if (!tables_args(c, a, o, n)) return kNoWorkspace;
+        return entry<int (*)(const bcg_cache*, int, const int32_t*, const int32_t*, int32_t*, void*)>(FORK)(
+            &a, n, list(c, o[5], "src", n), list(c, o[6], "dst", n), list(c, o[7], "granted", n), c.stream(o[8]));
+    });
+}
+// ..., rows, window, sinks, stream
+PyObject* free_(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+    NEED(9);
+    return guarded([&] {
+        Call c;
+        bcg_cache a{};
+        const int n = entries(c, o[5], "rows");
+        if (!tables_args(c, a, o, n)) return kNoWorkspace;
+        return entry<int (*)(const bcg_cache*, int, const int32_t*, int, int, void*)>(FREE)(
+            &a, n, list(c, o[5], "rows", n), integer(o[6], "window"), integer(o[7], "sinks"), c.stream(o[8]));
+    });
+}
+// ..., table_out, refs_out, moved, stream
+PyObject* compact(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+    NEED(9);
+    return guarded([&] {
+        Call c;
+        bcg_cache a{};
+        if (!tables_args(c, a, o, 0)) return kNoWorkspace;
+        int32_t* table = c.ptr<int32_t>(o[5], "table_out", I32, {a.rows, a.max_blocks});
+        int32_t* refs = c.ptr<int32_t>(o[6], "refs_out", I32, {a.num_pages});
+        return entry<int (*)(const bcg_cache*, int32_t*, int32_t*, int32_t*, void*)>(COMPACT)(
+            &a, table, refs, c.opt<int32_t>(o[7], "moved", I32, {1}), c.stream(o[8]));
+    });
+}
+// pool, src, dst, stream
+PyObject* copy(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+    NEED(4);
+    return guarded([&] {
+        Call c;
+        bcg_cache a{};
+        pool_args(c, a, o[0]);
+        const int n = entries(c, o[1], "src");
+        return entry<int (*)(const bcg_cache*, int, const int32_t*, const int32_t*, void*)>(COPY)(
+            &a, n, list(c, o[1], "src", n), list(c, o[2], "dst", n), c.stream(o[3]));
+    });
+}
+
+// An int32 [n, width] tensor or None.
+const int32_t* wide(Call& c, PyObject* o, const char* name, int64_t n, int32_t& width) {
+    width = 0;
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = c.whole(o, name, I32, {n, -1});
+    width = i32(t.size(1), name);
+    return static_cast<const int32_t*>(t.data_ptr());
+}
+
+// logits, out, cond_row, uncond_row, scale, history, history_len, prompt_len, repetition, presence, frequency, bias_ids,
+// bias, temperature, mask, stream
+PyObject* logits(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+    NEED(16);
+    return guarded([&] {
+        Call c;
+        bcg_logits_args a{};
+        const at::Tensor& x = c.rows(o[0], "logits", 2, a.logit_stride);
+        const at::Tensor& y = c.rows(o[1], "out", 2, a.out_stride);
+        a.dtype = storage(x, "logits");
+        a.out_dtype = storage(y, "out");
+        a.logits = x.data_ptr();
+        a.out = y.data_ptr();
+        a.logit_rows = i32(x.size(0), "logits");
+        a.n = i32(y.size(0), "out");
+        a.vocab = i32(y.size(1), "out");
+        if (x.size(1) != a.vocab) refuse("logits of %lld tokens, out of %d", (long long)x.size(1), a.vocab);
+        const int64_t n = a.n;
+        a.cond_row = c.ptr<const int32_t>(o[2], "cond_row", I32, {n});
+        a.uncond_row = c.opt<const int32_t>(o[3], "uncond_row", I32, {n});
+        a.scale = c.opt<const float>(o[4], "scale", F32, {n});
+        a.history = wide(c, o[5], "history", n, a.max_history);
+        a.history_len = c.opt<const int32_t>(o[6], "history_len", I32, {n});
+        a.prompt_len = c.opt<const int32_t>(o[7], "prompt_len", I32, {n});
+        a.repetition = c.opt<const float>(o[8], "repetition", F32, {n});
+        a.presence = c.opt<const float>(o[9], "presence", F32, {n});
+        a.frequency = c.opt<const float>(o[10], "frequency", F32, {n});
+        a.bias_ids = wide(c, o[11], "bias_ids", n, a.num_biases);
+        if ((o[11] == Py_None) != (o[12] == Py_None)) refuse("bias and bias_ids go together");
+        a.bias = c.opt<const float>(o[12], "bias", F32, {n, a.num_biases});
+        a.temperature = c.opt<const float>(o[13], "temperature", F32, {n});
+        a.mask = wide(c, o[14], "mask", n, a.mask_words);
+        return entry<int (*)(const bcg_logits_args*, void*)>(LOGITS)(&a, c.stream(o[15]));
+    });
+}
+
+// raw_stream, then the addresses of the library's entries in the order of the enumeration above
+PyObject* setup(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+    NEED(1 + ENTRIES);
+    for (int i = 0; i < ENTRIES; ++i) {
+        g_entry[i] = PyLong_AsVoidPtr(o[1 + i]);
+        if (!g_entry[i]) {
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an entry of the library is missing");
+            return nullptr;
+        }
+    }
+    Py_INCREF(o[0]);
+    Py_XDECREF(g_raw_stream);
+    g_raw_stream = o[0];
+    Py_RETURN_NONE;
+}
+
+#define M(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
+PyMethodDef g_methods[] = {M("setup", setup), M("attention", attention), M("append", append), M("extend", extend), M("fork", fork),
+                           M("free", free_), M("compact", compact), M("copy", copy), M("logits", logits), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_bind", "Argument checks and marshalling of the decoding calls.", -1, g_methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__bind() { return PyModule_Create(&g_module); }

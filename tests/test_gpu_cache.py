@@ -258,7 +258,7 @@ def test_step_captured_into_a_graph_and_replayed():
     b = Both([40, 33, 90, 12], spare=12)
     done, src, one = i32([1, 3]), i32([0, 2]), i32([1, 1])
     ok1, ok2 = torch.zeros_like(done), torch.zeros_like(done)
-    b.cache._args(4)  # the workspace is there before the capture
+    b.cache.reserve(4)  # the workspace is there before the capture
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     g = torch.cuda.CUDAGraph()
