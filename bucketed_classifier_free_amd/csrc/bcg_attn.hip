@@ -25,7 +25,7 @@ namespace {
 #define DG 4096
 #endif
 #ifndef NB8
-#define NB8 24
+#define NB8 12
 #endif
 #ifndef LB
 #define LB 64
@@ -127,7 +127,9 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     }
     nb = nb < 1 ? 1 : nb;
     const int64_t groups = (int64_t)(prompt ? (a->tokens * (int64_t)p.G + C - 1) / C + a->rows : (int64_t)a->rows * p.tiles) * p.kvh;
-    const int64_t aim = prompt ? kPromptGroups : kDecodeGroups;
+    // (in fp32 a prompt's tile takes several times as long: twice as many splits)
+    const bool slow = prompt && a->q_dtype == BCG_F32;
+    const int64_t aim = !prompt ? kDecodeGroups : slow ? 2 * kPromptGroups : kPromptGroups, least = slow ? kMinBlocks / 2 : kMinBlocks;
     int64_t splits = groups >= aim ? 1 : aim / groups;
     if (!prompt) {
         // half of the aim is enough where the splits would get shorter than 64 blocks
@@ -137,7 +139,7 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
         if (nb <= NB8 && groups < 1024 && a->q_dtype == BCG_BF16 && a->head_dim <= 128) splits = 1, p.waves = 8;
     }
     if (splits > kMaxSplits) splits = kMaxSplits;
-    if (splits > (nb + kMinBlocks - 1) / kMinBlocks) splits = (nb + kMinBlocks - 1) / kMinBlocks;
+    if (splits > (nb + least - 1) / least) splits = (nb + least - 1) / least;
     p.chunk = (int)((nb + splits - 1) / splits);
     p.splits = (int)((nb + p.chunk - 1) / p.chunk);
     const int64_t entries = (int64_t)a->tokens * a->q_heads;

@@ -14,7 +14,6 @@
 namespace bcg {
 namespace {
 
-constexpr int NT = 1024;  // lanes of the bookkeeping workgroup
 
 // ---------------------------------------------------------------- append
 
@@ -49,21 +48,51 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p, int s
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (id >> shift >= p.tokens) return;
     const int tok = (int)(id >> shift), lanes = 1 << shift;
+    const QT* k = static_cast<const QT*>(p.k) + (int64_t)tok * p.ks;
+    const QT* v = static_cast<const QT*>(p.v) + (int64_t)tok * p.vs;
+    Chunk<QT> x[2][2];
+    auto get = [&](int c0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int c = c0 + u * lanes;
+            if (c < p.chunks) {
+                x[u][0] = *reinterpret_cast<const Chunk<QT>*>(k + c * 8);
+                x[u][1] = *reinterpret_cast<const Chunk<QT>*>(v + c * 8);
+            }
+        }
+    };
+    int c0 = (int)id & (lanes - 1);
+    get(c0);  // on their way while the token's place is found
     int row = tok, pos = 1;
     if (p.off) {
         // the row whose run holds the token: the last one that begins at or before it
-        int a = 0, b = p.rows;  // off[a] <= tok, off[b] > tok
-        if (p.off[0] > tok || p.off[p.rows] <= tok) return;
-        while (b - a > 1) {
-            const int mid = (a + b) >> 1;
-            if (p.off[mid] <= tok) a = mid;
-            else b = mid;
+        int a = 0, b = p.rows;  // off[a] <= tok < off[b]
+        const int g = min((int)((int64_t)tok * p.rows / p.tokens), p.rows - 1);  // runs of like lengths: at once
+        const int first = p.off[0], end = p.off[p.rows], at = p.off[g], next = p.off[g + 1];
+        if (first > tok || end <= tok) return;
+        if (at <= tok && tok < next) {
+            a = g;
+            b = g + 1;
+        }
+        if (shift == 6) {
+            // a wave's token: 64 places of the range at a time
+            const int lane = (int)id & 63;
+            while (b - a > 1) {
+                const int step = (b - a + 63) >> 6, i = a + lane * step;
+                const uint64_t le = __ballot(i < b && p.off[min(i, b)] <= tok);
+                a += (__popcll(le) - 1) * step;  // lane 0's is always one of them
+                b = min(a + step, b);
+            }
+        } else {
+            while (b - a > 1) {
+                const int mid = (a + b) >> 1;
+                if (p.off[mid] <= tok) a = mid;
+                else b = mid;
+            }
         }
         row = a;
         pos = p.off[row + 1] - tok;
     }
-    const QT* k = static_cast<const QT*>(p.k) + (int64_t)tok * p.ks;
-    const QT* v = static_cast<const QT*>(p.v) + (int64_t)tok * p.vs;
     pos = min(max(p.len[row], 0), p.maxb * p.ps) - pos;
     if (pos < 0) return;
     const int blk = pos / p.ps, pg = p.table[(int64_t)row * p.maxb + blk];
@@ -88,16 +117,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p, int s
             for (int i = 0; i < (int)sizeof(QT) / 2; ++i) reinterpret_cast<u32x4_t*>(static_cast<QT*>(cache) + at)[i] = x.w[i];
         }
     };
-    for (int c0 = (int)id & (lanes - 1); c0 < p.chunks; c0 += 2 * lanes) {
-        Chunk<QT> x[2][2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int c = c0 + u * lanes;
-            if (c < p.chunks) {
-                x[u][0] = *reinterpret_cast<const Chunk<QT>*>(k + c * 8);
-                x[u][1] = *reinterpret_cast<const Chunk<QT>*>(v + c * 8);
-            }
-        }
+    while (c0 < p.chunks) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int c = c0 + u * lanes, h = c * 8 / p.D, d = c * 8 - h * p.D;
@@ -106,6 +126,8 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p, int s
                 put(p.vc, (int64_t)pg * p.vps, p.vscale, h, d, x[u][1]);
             }
         }
+        c0 += 2 * lanes;
+        get(c0);
     }
 }
 
@@ -113,7 +135,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p, int s
 
 // Sum over the lanes before this one, of one value per lane; `total` gets the
 // workgroup's sum.  Two barriers; ws: NT / 64 words of LDS.
-template <typename I> __device__ __forceinline__ I scan_excl(I x, I* ws, I& total) {
+template <int NT, typename I> __device__ __forceinline__ I scan_excl(I x, I* ws, I& total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     I s = x;
 #pragma unroll
@@ -155,14 +177,15 @@ __device__ __forceinline__ uint32_t live_pages(const int32_t* refs, int np, int 
 }
 
 // The lowest `want` free pages, ascending, into `fresh`; the count of free
-// pages if it is below `want`, else any number >= want.
-__device__ int find_free(const int32_t* refs, int np, int want, int32_t* fresh, int* ws) {
+// pages if it is below `want`, else any number >= want.  live0: live_pages of
+// the lane's first range, which the caller has asked for early.
+template <int NT> __device__ int find_free(const int32_t* refs, int np, int want, uint32_t live0, int32_t* fresh, int* ws) {
     int found = 0;
     for (int base = 0; base < np && found < want; base += NT * kRefs) {
         const int i = base + threadIdx.x * kRefs;
-        const uint32_t live = live_pages(refs, np, i);
+        const uint32_t live = base ? live_pages(refs, np, i) : live0;
         int total;
-        int at = found + scan_excl((int)__popc(~live & (kRefs >= 32 ? ~0u : (1u << kRefs) - 1u)), ws, total);
+        int at = found + scan_excl<NT>((int)__popc(~live & ((1u << kRefs) - 1u)), ws, total);
 #pragma unroll
         for (int j = 0; j < kRefs; ++j)
             if (!(live >> j & 1u)) {
@@ -190,60 +213,100 @@ struct CacheParams {
     int32_t* pair;   // [2n or 2 num_pages] pages to copy: from, to
 };
 
-// owner[row] = the first entry of the list that names it.
-__device__ void first_entries(const CacheParams& p, int n, const int32_t* list) {
-    for (int i = threadIdx.x; i < n; i += NT)
-        if (list[i] >= 0 && list[i] < p.rows) p.owner[list[i]] = n;
+constexpr int kRowsLds = 4096, kFreshLds = 4096;
+
+// What the bookkeeping workgroup keeps in LDS while it fits (a step of a batch
+// always does: a round trip to memory costs as much as all the arithmetic).
+template <int NT> struct Book {
+    int owner[kRowsLds];  // the first list entry that names the row
+    int fresh[kFreshLds];
+    int ws[NT / 64];
+    int64_t ws64[NT / 64];
+};
+
+// Whether entry i of the list (of value `row`) is the first to name its row.
+// Every lane calls it for its first entry before any looks at the others'.
+template <int NT> __device__ void first_entries(const CacheParams& p, Book<NT>& bk, int n, const int32_t* list, int row0) {
+    const bool lds = p.rows <= kRowsLds;
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const int r = i < NT ? row0 : list[i];
+        if (r >= 0 && r < p.rows) (lds ? bk.owner[r] : p.owner[r]) = n;
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += NT)
-        if (list[i] >= 0 && list[i] < p.rows) atomicMin(&p.owner[list[i]], i);
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const int r = i < NT ? row0 : list[i];
+        if (r >= 0 && r < p.rows) {
+            if (lds) atomicMin(&bk.owner[r], i);
+            else atomicMin(&p.owner[r], i);
+        }
+    }
     __syncthreads();
+}
+template <int NT> __device__ __forceinline__ bool is_first(const CacheParams& p, const Book<NT>& bk, int row, int i) {
+    return (p.rows <= kRowsLds ? bk.owner[row] : p.owner[row]) == i;
 }
 
 __device__ __forceinline__ int row_len(const CacheParams& p, int row) { return min(max(p.len[row], 0), p.maxb * p.ps); }
 
 // ---------------------------------------------------------------- extend, fork
 
-__global__ void __launch_bounds__(NT) extend_kernel(const CacheParams p, int n, const int32_t* rows, const int32_t* count, int32_t* granted) {
-    __shared__ int ws[NT / 64];
-    __shared__ int64_t ws64[NT / 64];  // a list's needs can pass 32 bits
-    first_entries(p, n, rows);
-    int64_t want = 0;
-    for (int base = 0; base < n; base += NT) {
-        const int i = base + threadIdx.x;
-        int need = 0, ok = 0;
-        if (i < n && rows[i] >= 0 && rows[i] < p.rows && p.owner[rows[i]] == i && count[i] >= 0) {
-            const int len = row_len(p, rows[i]);
-            const int64_t to = (int64_t)len + count[i];
-            if (to <= (int64_t)p.maxb * p.ps) {
-                ok = 1;
-                need = (int)((to + p.ps - 1) / p.ps) - (len + p.ps - 1) / p.ps;
-            }
+// Entry i's row, old length and pages needed live in the registers of lane i %
+// NT for the first NT entries, and are worked out again for those behind them.
+template <int NT> __global__ void __launch_bounds__(NT) extend_kernel(const CacheParams p, int n, const int32_t* rows, const int32_t* count, int32_t* granted) {
+    __shared__ Book<NT> bk;
+    const int tid = threadIdx.x;
+    const int row0 = tid < n ? rows[tid] : -1, count0 = tid < n ? count[tid] : -1;
+    const uint32_t live0 = live_pages(p.refs, p.np, tid * kRefs);
+    const int len0 = row0 >= 0 && row0 < p.rows ? row_len(p, row0) : 0;
+    first_entries(p, bk, n, rows, row0);
+    // pages that entry i needs, -1: refused
+    auto needs = [&](int i, int row, int add, int len) -> int {
+        if (i >= n || row < 0 || row >= p.rows || add < 0 || !is_first(p, bk, row, i)) return -1;
+        const int64_t to = (int64_t)len + add;
+        return to > (int64_t)p.maxb * p.ps ? -1 : (int)((to + p.ps - 1) / p.ps) - (len + p.ps - 1) / p.ps;
+    };
+    auto at_entry = [&](int i, int& row, int& add, int& len) {
+        if (i < NT) {
+            row = row0; add = count0; len = len0;
+        } else {
+            row = i < n ? rows[i] : -1;
+            add = i < n ? count[i] : -1;
+            len = row >= 0 && row < p.rows ? row_len(p, row) : 0;
         }
+    };
+    int64_t want = 0;  // a list's needs can pass 32 bits
+    for (int base = 0; base < n; base += NT) {
+        int row, add, len;
+        at_entry(base + tid, row, add, len);
+        const int need = needs(base + tid, row, add, len);
         int64_t total;
-        scan_excl<int64_t>(need, ws64, total);
-        if (i < n) p.need[i] = ok ? need : -1;
+        scan_excl<NT, int64_t>(max(need, 0), bk.ws64, total);
         want += total;
+        if (n > NT && base + tid < n) p.need[base + tid] = need;  // lengths change below
     }
-    const int found = find_free(p.refs, p.np, (int)min(want, (int64_t)p.np), p.fresh, ws);
+    const int asked = (int)min(want, (int64_t)p.np);
+    int32_t* fresh = asked <= kFreshLds ? bk.fresh : p.fresh;
+    const int found = asked ? find_free<NT>(p.refs, p.np, asked, live0, fresh, bk.ws) : 0;
     int64_t before = 0;
     for (int base = 0; base < n; base += NT) {
-        const int i = base + threadIdx.x;
-        const int need = i < n ? p.need[i] : -1;
+        const int i = base + tid;
+        int row, add, len;
+        at_entry(i, row, add, len);
+        const int need = n > NT ? (i < n ? p.need[i] : -1) : needs(i, row, add, len);
         int64_t total;
-        const int64_t at = before + scan_excl<int64_t>(max(need, 0), ws64, total);
+        const int64_t at = before + scan_excl<NT, int64_t>(max(need, 0), bk.ws64, total);
         before += total;
         if (i < n) {
             const bool ok = need >= 0 && (need == 0 || at + need <= found);
             granted[i] = ok;
             if (ok) {
-                const int row = rows[i], len = row_len(p, row), b = (len + p.ps - 1) / p.ps;
+                const int b = (len + p.ps - 1) / p.ps;
                 for (int k = 0; k < need; ++k) {
-                    const int pg = p.fresh[at + k];
+                    const int pg = fresh[at + k];
                     p.table[(int64_t)row * p.maxb + b + k] = pg;
                     p.refs[pg] = 1;
                 }
-                p.len[row] = len + count[i];
+                p.len[row] = len + add;
             }
         }
     }
@@ -252,45 +315,54 @@ __global__ void __launch_bounds__(NT) extend_kernel(const CacheParams p, int n, 
 // Which forks go ahead, and the page of each one's partly filled last block.
 // Leaves pair[2i] = page to copy or -1, pair[2i + 1] = where to, need[i] = -1
 // where refused, else the length.
-__global__ void __launch_bounds__(NT) fork_kernel(const CacheParams p, int n, const int32_t* src, const int32_t* dst, int32_t* granted) {
-    __shared__ int ws[NT / 64];
-    first_entries(p, n, dst);
-    int want = 0;
+template <int NT> __global__ void __launch_bounds__(NT) fork_kernel(const CacheParams p, int n, const int32_t* src, const int32_t* dst, int32_t* granted) {
+    __shared__ Book<NT> bk;
+    const int tid = threadIdx.x;
+    const int src0 = tid < n ? src[tid] : -1, dst0 = tid < n ? dst[tid] : -1;
+    const uint32_t live0 = live_pages(p.refs, p.np, tid * kRefs);
+    first_entries(p, bk, n, dst, dst0);
+    // entry i: the source's length (-1: refused) and its partly filled page (-1: none)
+    auto look = [&](int i, int& len, int& part) {
+        len = part = -1;
+        if (i >= n) return;
+        const int s = i < NT ? src0 : src[i], d = i < NT ? dst0 : dst[i];
+        if (s < 0 || s >= p.rows || d < 0 || d >= p.rows || s == d || !is_first(p, bk, d, i)) return;
+        const int from = row_len(p, s), blk = min(from / p.ps, max(p.maxb - 1, 0));
+        const int page = p.maxb > 0 ? p.table[(int64_t)s * p.maxb + blk] : -1, old = p.len[d];
+        const int head = p.maxb > 0 ? p.table[(int64_t)d * p.maxb] : -1;
+        if (old != 0 || head >= 0) return;
+        len = from;
+        if (from % p.ps && page >= 0 && page < p.np) part = page;
+    };
+    int want = 0, len0 = -1, part0 = -1;
     for (int base = 0; base < n; base += NT) {
-        const int i = base + threadIdx.x;
-        int len = -1, part = -1;
-        if (i < n) {
-            const int s = src[i], d = dst[i];
-            if (s >= 0 && s < p.rows && d >= 0 && d < p.rows && s != d && p.owner[d] == i && p.len[d] == 0 &&
-                (p.maxb == 0 || p.table[(int64_t)d * p.maxb] < 0)) {
-                len = row_len(p, s);
-                if (len % p.ps) part = p.table[(int64_t)s * p.maxb + len / p.ps];
-                if (part >= p.np) part = -1;
-            }
-            p.need[i] = len;
-            p.pair[2 * i] = part;
+        int len, part, total;
+        look(base + tid, len, part);
+        if (base == 0) {
+            len0 = len;
+            part0 = part;
         }
-        int total;
-        scan_excl(part >= 0 ? 1 : 0, ws, total);
+        scan_excl<NT>(part >= 0 ? 1 : 0, bk.ws, total);
         want += total;
     }
-    const int found = find_free(p.refs, p.np, min(want, p.np), p.fresh, ws);
+    const int asked = min(want, p.np);
+    int32_t* fresh = asked <= kFreshLds ? bk.fresh : p.fresh;
+    const int found = asked ? find_free<NT>(p.refs, p.np, asked, live0, fresh, bk.ws) : 0;
     int before = 0;
     for (int base = 0; base < n; base += NT) {
-        const int i = base + threadIdx.x;
-        const int len = i < n ? p.need[i] : -1, part = i < n ? p.pair[2 * i] : -1;
-        int total;
-        const int at = before + scan_excl(part >= 0 ? 1 : 0, ws, total);
+        const int i = base + tid;
+        int len = len0, part = part0, total;
+        if (base) look(i, len, part);
+        const int at = before + scan_excl<NT>(part >= 0 ? 1 : 0, bk.ws, total);
         before += total;
         if (i < n) {
             const bool ok = len >= 0 && (part < 0 || at < found);
             granted[i] = ok;
-            if (!ok) {
-                p.need[i] = -1;
-                p.pair[2 * i] = -1;
-            } else if (part >= 0) {
-                p.pair[2 * i + 1] = p.fresh[at];
-                p.refs[p.fresh[at]] = 1;
+            p.need[i] = ok ? len : -1;
+            p.pair[2 * i] = ok ? part : -1;
+            if (ok && part >= 0) {
+                p.pair[2 * i + 1] = fresh[at];
+                p.refs[fresh[at]] = 1;
             }
         }
     }
@@ -368,7 +440,7 @@ __global__ void __launch_bounds__(256) free_kernel(const CacheParams p, const in
 
 // The moves: fresh[p] = new place of page p; pair[2k], pair[2k + 1] = from, to
 // of move k; owner[0] = their count (rows >= 1) -- kept in pair's last word.
-__global__ void __launch_bounds__(NT) compact_plan_kernel(const CacheParams p, int32_t* refs_out, int32_t* moved) {
+template <int NT> __global__ void __launch_bounds__(NT) compact_plan_kernel(const CacheParams p, int32_t* refs_out, int32_t* moved) {
     __shared__ int ws[NT / 64];
     __shared__ int64_t ws64[NT / 64];
     constexpr uint32_t kMask = (1u << kRefs) - 1u;
@@ -378,7 +450,7 @@ __global__ void __launch_bounds__(NT) compact_plan_kernel(const CacheParams p, i
     for (int base = 0; base < p.np; base += NT * kRefs) {
         const int i = base + threadIdx.x * kRefs;
         int total;
-        scan_excl((int)__popc(live_pages(p.refs, p.np, i) & below(i, p.np)), ws, total);
+        scan_excl<NT>((int)__popc(live_pages(p.refs, p.np, i) & below(i, p.np)), ws, total);
         live += total;
     }
     int holes = 0, movers = 0;
@@ -387,7 +459,7 @@ __global__ void __launch_bounds__(NT) compact_plan_kernel(const CacheParams p, i
         const uint32_t l = live_pages(p.refs, p.np, i), hole = ~l & below(i, live), mover = l & below(i, p.np) & ~below(i, live);
         // both sums in one scan
         int64_t total;
-        const int64_t before = scan_excl((int64_t)__popc(hole) << 32 | (int64_t)__popc(mover), ws64, total);
+        const int64_t before = scan_excl<NT>((int64_t)__popc(hole) << 32 | (int64_t)__popc(mover), ws64, total);
         int ah = holes + (int)(before >> 32), am = movers + (int)(uint32_t)before;
         holes += (int)(total >> 32);
         movers += (int)(uint32_t)total;
@@ -447,6 +519,10 @@ __global__ void __launch_bounds__(256) copy_kernel(const CacheParams p, int n, c
 }
 
 // ---------------------------------------------------------------- host
+
+// Lanes of the bookkeeping workgroup: 256 take a list and a pool of ordinary
+// size in one go, and meet at a barrier sooner than 1024 do.
+bool small_book(const CacheParams& p, int n) { return n <= 256 && p.np <= 256 * kRefs; }
 
 constexpr int64_t kCopyGroups = 256 * 8;  // one resident round of copying workgroups
 
@@ -551,7 +627,9 @@ extern "C" int cache_extend(const bcg_cache* c, int n, const int32_t* rows, cons
     if (rc != BCG_OK) return rc;
     if (n == 0) return BCG_OK;
     if (!rows || !count || !granted) return fail(BCG_EINVAL, "cache_extend: NULL list");
-    hipLaunchKernelGGL(extend_kernel, dim3(1), dim3(NT), 0, static_cast<hipStream_t>(stream), p, n, rows, count, granted);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (small_book(p, n)) hipLaunchKernelGGL(extend_kernel<256>, dim3(1), dim3(256), 0, st, p, n, rows, count, granted);
+    else hipLaunchKernelGGL(extend_kernel<1024>, dim3(1), dim3(1024), 0, st, p, n, rows, count, granted);
     return hip_status(hipGetLastError(), "cache_extend: launch");
 }
 
@@ -563,7 +641,8 @@ extern "C" int cache_fork(const bcg_cache* c, int n, const int32_t* src, const i
     if (n == 0) return BCG_OK;
     if (!src || !dst || !granted) return fail(BCG_EINVAL, "cache_fork: NULL list");
     hipStream_t st = static_cast<hipStream_t>(stream);
-    hipLaunchKernelGGL(fork_kernel, dim3(1), dim3(NT), 0, st, p, n, src, dst, granted);
+    if (small_book(p, n)) hipLaunchKernelGGL(fork_kernel<256>, dim3(1), dim3(256), 0, st, p, n, src, dst, granted);
+    else hipLaunchKernelGGL(fork_kernel<1024>, dim3(1), dim3(1024), 0, st, p, n, src, dst, granted);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess) {
         hipLaunchKernelGGL(fork_copy_kernel, dim3(n + copy_groups(p, n)), dim3(256), 0, st, p, n, src, dst);
@@ -599,7 +678,7 @@ extern "C" int cache_compact(const bcg_cache* c, int32_t* table_out, int32_t* re
         any_overlap(p.refs, rb, table_out, tb))
         return fail(BCG_EINVAL, "%s: outputs overlap the tables in part", who);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    hipLaunchKernelGGL(compact_plan_kernel, dim3(1), dim3(NT), 0, st, p, refs_out, moved);
+    hipLaunchKernelGGL(compact_plan_kernel<1024>, dim3(1), dim3(1024), 0, st, p, refs_out, moved);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess) {
         const int64_t t = ((int64_t)p.rows * p.maxb + 255) / 256;

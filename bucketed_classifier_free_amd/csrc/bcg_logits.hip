@@ -95,10 +95,16 @@ template <typename T, typename OT, bool SPARSE>
 __global__ void __launch_bounds__(NT) logits_kernel(const LogitsParams p) {
     __shared__ __attribute__((aligned(16))) uint32_t word[SPARSE ? kSeg : 4];
     const int i = blockIdx.y, s0 = blockIdx.x * kSeg, tid = threadIdx.x;
+    // everything that the sample's row asks for is requested at once
     const int cr = p.cond[i];
-    if (cr < 0 || cr >= p.rows) return;
     const float w = p.scale ? p.scale[i] : 1.0f;
     int ur = p.uncond ? p.uncond[i] : -1;
+    const int hl = SPARSE && p.history ? min(max(p.hlen[i], 0), p.hist) : 0, pl = SPARSE && p.plen ? p.plen[i] : 0;
+    const float rep = p.rep ? p.rep[i] : 1.0f, pres = p.pres ? p.pres[i] : 0.0f, freq = p.freq ? p.freq[i] : 0.0f;
+    const float cool = p.temp ? 1.0f / p.temp[i] : 1.0f;
+    const int32_t* bias_ids = p.bias_ids + (int64_t)i * p.biases;
+    const int bias0 = SPARSE && p.bias_ids && tid < p.biases ? bias_ids[tid] : -1;
+    if (cr < 0 || cr >= p.rows) return;
     if (ur >= p.rows) ur = -1;
     const bool guided = ur >= 0 && w != 1.0f;
     const T* crow = static_cast<const T*>(p.logits) + (int64_t)cr * p.stride;
@@ -112,7 +118,6 @@ __global__ void __launch_bounds__(NT) logits_kernel(const LogitsParams p) {
         if (guided) load8<T>(urow + j, p.vocab - j, u[r]);
     }
     if constexpr (SPARSE) {
-        const int hl = p.history ? min(max(p.hlen[i], 0), p.hist) : 0, pl = p.plen ? p.plen[i] : 0;
         const int32_t* h = p.history + (int64_t)i * p.hist;
         constexpr int U = 8;  // entries of a lane on their way
         int e[U];
@@ -135,9 +140,8 @@ __global__ void __launch_bounds__(NT) logits_kernel(const LogitsParams p) {
             }
         }
         if (p.bias_ids) {
-            const int32_t* b = p.bias_ids + (int64_t)i * p.biases;
             for (int k = tid; k < p.biases; k += NT) {
-                const int id = b[k];
+                const int id = k < NT ? bias0 : bias_ids[k];
                 if (id < s0 || id - s0 >= kSeg) continue;
                 uint32_t old = word[id - s0];
                 while ((old & kBiasMask) < (uint32_t)k + 1u) {
@@ -149,8 +153,6 @@ __global__ void __launch_bounds__(NT) logits_kernel(const LogitsParams p) {
         }
         __syncthreads();
     }
-    const float rep = p.rep ? p.rep[i] : 1.0f, pres = p.pres ? p.pres[i] : 0.0f, freq = p.freq ? p.freq[i] : 0.0f;
-    const float cool = p.temp ? 1.0f / p.temp[i] : 1.0f;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
         const int j = s0 + (r * NT + tid) * kVec, left = p.vocab - j;

@@ -1,0 +1,168 @@
+"""Guided decoding of a small token model, end to end on one GPU.
+
+A random two-layer transformer answers a few requests under bucketed
+classifier-free guidance: every sample has a conditional row and, while its
+bucket's scale is not 1, an unconditional one, both in one paged cache.  The
+samples of a request share its prompt: the prompt runs once (prompt_attention,
+with a sliding window and two sinks), its rows are forked, and each decoding
+step appends one token a row (cache_extend, cache_append), attends over the
+pages (paged_attention) and combines the branches' logits with penalties and a
+grammar mask (guided_logits).  When a sample's scale falls to 1 its
+unconditional row gives its pages back (cache_free), pages behind the window
+are given back too, and now and then the pool is compacted.
+
+    python3 examples/guided_decode.py [--steps N] [--dtype bf16|f32] [--cache e4m3]
+"""
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import bucketed_classifier_free_amd as bcg  # noqa: E402
+
+LAYERS, HEADS, KV_HEADS, DIM, VOCAB, WINDOW, SINKS = 2, 8, 2, 64, 1003, 48, 2
+
+
+class Model:
+    def __init__(self, dtype, seed=0):
+        g = torch.Generator().manual_seed(seed)
+        rand = lambda *s: (torch.randn(s, generator=g) / s[0] ** 0.5).to(dtype).cuda()  # noqa: E731
+        width = HEADS * DIM
+        self.embed = rand(VOCAB, width) * VOCAB ** 0.5
+        self.qkv = [rand(width, (HEADS + 2 * KV_HEADS) * DIM) for _ in range(LAYERS)]
+        self.out = [rand(width, width) for _ in range(LAYERS)]
+        self.up = [rand(width, 2 * width) for _ in range(LAYERS)]
+        self.down = [rand(2 * width, width) for _ in range(LAYERS)]
+        self.head = rand(width, VOCAB)
+
+    @staticmethod
+    def norm(x):
+        y = x.float()
+        return (y * torch.rsqrt(y.square().mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
+
+    def __call__(self, tokens, attend):
+        """Logits of ``tokens``; attend(layer, q, k, v) -> attention output."""
+        x = self.embed[tokens.long()]
+        for layer in range(LAYERS):
+            qkv = (self.norm(x) @ self.qkv[layer]).view(len(tokens), HEADS + 2 * KV_HEADS, DIM)
+            q, k, v = qkv[:, :HEADS], qkv[:, HEADS:HEADS + KV_HEADS], qkv[:, HEADS + KV_HEADS:]
+            x = x + attend(layer, q, k, v).flatten(1) @ self.out[layer]
+            x = x + torch.relu(self.norm(x) @ self.up[layer]) @ self.down[layer]
+        return self.norm(x) @ self.head
+
+
+class Decoder:
+    """``samples`` answers a request; rows [0, samples) of the cache are the
+    unconditional branches, rows [samples, 2 samples) the conditional ones."""
+
+    def __init__(self, model, samples, steps, dtype, cache_dtype, bucket_cfg, page=16, pages=96):
+        self.m, self.n, self.steps, self.dtype = model, samples, steps, dtype
+        self.table = bucket_cfg
+        self.rows = 2 * samples
+        self.cache = bcg.PagedCache.empty(LAYERS, pages, KV_HEADS, page, DIM, self.rows, 16, dtype=cache_dtype)
+        self.scale8 = torch.full((KV_HEADS,), 0.05, device="cuda") if cache_dtype == torch.float8_e4m3fn else None
+        self.work = bcg.attention_workspace(256, HEADS, DIM)
+        self.history = torch.zeros((samples, 256), dtype=torch.int32, device="cuda")
+
+    def i32(self, v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+    def attend(self, offset):
+        c = self.cache
+        eight = dict(k_scale=self.scale8, v_scale=self.scale8)
+
+        def layer_attention(layer, q, k, v):
+            out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+            bcg.cache_append(k, v, c.keys(layer), c.values(layer), c.table, c.length, offset=offset, **eight)
+            kw = dict(workspace=self.work, window=WINDOW, sinks=SINKS, **eight)
+            bcg.prompt_attention(q, offset, c.keys(layer), c.values(layer), c.table, c.length, out, **kw)
+            return out
+
+        def decode_attention(layer, q, k, v):
+            out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+            bcg.cache_append(k, v, c.keys(layer), c.values(layer), c.table, c.length, **eight)
+            bcg.paged_attention(q, c.keys(layer), c.values(layer), c.table, c.length, out, workspace=self.work,
+                                window=WINDOW, sinks=SINKS, **eight)
+            return out
+
+        return layer_attention if offset is not None else decode_attention
+
+    def prompts(self, uncond, cond):
+        """The request's two prompts into rows 0 and n, forked to the others;
+        the logits [2, vocab] that follow them."""
+        n, lens = self.n, [len(uncond), len(cond)]
+        ok = bcg.cache_extend(self.cache, self.i32([0, n]), self.i32(lens))
+        offset = [0] * (self.rows + 1)
+        for r in range(self.rows):
+            offset[r + 1] = offset[r] + (lens[0] if r == 0 else lens[1] if r == n else 0)
+        tokens = self.i32(uncond + cond)
+        logits = self.m(tokens, self.attend(self.i32(offset)))
+        others = [r for r in range(self.rows) if r not in (0, n)]
+        ok2 = bcg.cache_fork(self.cache, self.i32([0 if r < n else n for r in others]), self.i32(others))
+        assert bool(ok.all()) and bool(ok2.all()), "the pool is too small"
+        self.prompt = cond
+        self.history[:, :len(cond)] = self.i32(cond)
+        return logits[[lens[0] - 1, lens[0] + lens[1] - 1]]
+
+    def run(self, uncond, cond, allowed=None, on_step=None):
+        """The samples' tokens [samples, steps]."""
+        n, length = self.n, len(cond)
+        logits = self.prompts(uncond, cond)
+        logits = logits.repeat_interleave(n, 0)  # all branches begin alike
+        rep = torch.full((n,), 1.2, device="cuda")
+        freq = torch.full((n,), 0.1, device="cuda")
+        temp = torch.linspace(0.7, 1.3, n, device="cuda")
+        alive = [True] * n  # unconditional rows that still hold pages
+        answer = []
+        for step in range(self.steps):
+            # samples are at different points of the guidance curve
+            at = [min(self.steps - 1, step + 2 * i) for i in range(n)]
+            plan = bcg.bcg_plan_build(at, self.steps, self.table)
+            need = [int(u) >= 0 for u in plan.uncond_row]
+            out = torch.empty((n, VOCAB), device="cuda")
+            kw = dict(history=self.history, history_len=self.i32([length + step] * n), prompt_len=self.i32([length] * n),
+                      repetition=rep, frequency=freq, temperature=temp, mask=allowed)
+            bcg.guided_logits(logits, out, self.i32([n + i for i in range(n)]),
+                              self.i32([i if need[i] else -1 for i in range(n)]), torch.from_numpy(plan.scale).cuda(), **kw)
+            if on_step:
+                on_step(self, step, logits, out, need, plan.scale, kw)
+            token = out.argmax(-1).int()
+            answer.append(token)
+            self.history[:, length + step] = token
+            gone = [i for i in range(n) if alive[i] and not need[i]]
+            if gone:
+                bcg.cache_free(self.cache, self.i32(gone))
+                alive = [a and i not in gone for i, a in enumerate(alive)]
+            if step % 16 == 15:
+                bcg.cache_free(self.cache, self.i32([r for r in range(self.rows)]), window=WINDOW, sinks=SINKS)
+                bcg.cache_compact(self.cache)
+            live = [i for i in range(n) if alive[i]] + list(range(n, 2 * n))
+            ok = bcg.cache_extend(self.cache, self.i32(live), self.i32([1] * len(live)))
+            assert bool(ok.all()), "the pool is too small"
+            # rows without pages ride along with length 0: their attention is zero, their logits unused
+            logits = self.m(token.repeat(2), self.attend(None))
+        bcg.cache_free(self.cache, self.i32(list(range(self.rows))))
+        return torch.stack(answer, 1)
+
+
+def main():
+    ap = argparse.ArgumentParser()
+    ap.add_argument("--steps", type=int, default=40)
+    ap.add_argument("--samples", type=int, default=4)
+    ap.add_argument("--dtype", choices=["bf16", "f32"], default="bf16")
+    ap.add_argument("--cache", choices=["same", "e4m3"], default="same")
+    a = ap.parse_args()
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[a.dtype]
+    curve = bcg.bucket_table("front_high", 3.0, 1.0, 0.6, 8)
+    d = Decoder(Model(dtype), a.samples, a.steps, dtype, torch.float8_e4m3fn if a.cache == "e4m3" else dtype, curve)
+    tokens = d.run(list(range(5, 12)), list(range(100, 175)))
+    for i, t in enumerate(tokens.tolist()):
+        print(f"sample {i}: {t}")
+    free = int((d.cache.refs <= 0).sum())
+    print(f"{free} of {d.cache.refs.numel()} pages free at the end")
+
+
+if __name__ == "__main__":
+    main()

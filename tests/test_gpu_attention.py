@@ -298,6 +298,60 @@ def test_prompt_and_decode_agree_with_one_query_a_row():
     check(*decode(c, x), ref, 128, 200, torch.bfloat16)
 
 
+def dense64(x, c, pos, scale, window=0):
+    """Attention of x [rows, new, heads, dim] at pos [new], heads == kv_heads,
+    in float64 on the GPU; (out, bounds as oracle.decode.attention)."""
+    rows, page = x.shape[0], c["k"].shape[2]
+    k, v = (c[n].double()[c["table"].long()].transpose(1, 2).flatten(2, 3) for n in ("k", "v"))  # [rows, heads, tokens, dim]
+    t = torch.arange(k.shape[2], device="cuda")
+    seen = (t <= pos[:, None]) & ((t > pos[:, None] - window) if window else True)
+    q = x.double().transpose(1, 2)
+    s = torch.matmul(q, k.transpose(-1, -2).contiguous()) * scale
+    s = s.masked_fill(~seen, -float("inf"))
+    p, lse = torch.softmax(s, -1), torch.logsumexp(s, -1)
+    v = torch.where((t <= int(pos.max()))[:, None], v, 0.0)
+    out, weight = torch.matmul(p, v), torch.matmul(p, v.abs())
+    reach = torch.matmul(q.abs(), torch.nan_to_num(k).abs().transpose(-1, -2).contiguous()).amax(-1) * scale
+    back = lambda y: y.transpose(1, 2).flatten(0, 1).cpu().numpy()  # noqa: E731
+    return back(out), back(lse), back(weight), back(reach)
+
+
+@pytest.mark.parametrize("q,kv", KINDS[:2])
+@pytest.mark.parametrize("window", [0, 700])
+def test_prompt_long_runs_without_splits(q, kv, window):
+    """More tiles in one workgroup than one read of the table covers."""
+    new, heads, dim = 1300, 32, 16
+    c = make_cache([new, new], heads, dim, 48, kv, seed=window, rot=0.0)
+    x = make_queries(2 * new, heads, dim, q, seed=1, strided=False)
+    ref = dense64(x.view(2, new, heads, dim), c, torch.arange(new, device="cuda"), 0.25, window)
+    check(*prompt(c, x, [0, new, 2 * new], window, 0, scale=0.25, max_new=new), ref, dim, new, TYPES[q])
+
+
+@pytest.mark.parametrize("q,kv", KINDS[:2])
+def test_decode_many_rows_without_splits(q, kv):
+    """A workgroup that walks a whole long row, more blocks than one read of
+    the table covers; rows share pages."""
+    rows, heads, dim, n = 520, 8, 16, 4500
+    c = make_cache([n], heads, dim, 16, kv, seed=2, rot=0.0, extra_blocks=0)
+    order = torch.stack([torch.randperm(282, generator=torch.Generator().manual_seed(r)) for r in range(rows)])
+    # the partly filled page stays last
+    full = c["table"][0, :281].cpu()
+    order = torch.cat([full[order[order < 281].view(rows, 281)], c["table"][0, 281:].cpu().expand(rows, 1)], 1)
+    c["table"] = order.int().contiguous().cuda()
+    c["length"] = torch.full((rows,), n, dtype=torch.int32, device="cuda")
+    x = make_queries(rows, heads, dim, q, seed=5)
+    ref = dense64(x[:, None], c, torch.tensor([n - 1], device="cuda"), 0.25)
+    check(*decode(c, x), ref, dim, n, TYPES[q])
+
+
+def test_decode_many_short_rows():
+    rng = np.random.default_rng(1)
+    lens = [int(n) for n in rng.integers(0, 50, 600)]
+    c = make_cache(lens, 8, 64, 16, "bf16", seed=3)
+    x = make_queries(600, 8, 64, "bf16", seed=3)
+    check(*decode(c, x), reference(x, np.arange(601), c, 0.125, 0, 0), 64, 50, torch.bfloat16)
+
+
 def test_on_another_stream_and_in_a_graph():
     import bucketed_classifier_free_amd as bcg
     lens = [900, 77]

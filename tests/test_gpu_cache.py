@@ -59,6 +59,26 @@ def test_append(q, kv, new, past, layout):
     assert np.array_equal(bits(c["k"]), bits(want_k)) and np.array_equal(bits(c["v"]), bits(want_v))
 
 
+@pytest.mark.parametrize("heads,dim", [(1, 8), (1, 64), (8, 128)])
+@pytest.mark.parametrize("rows", [1, 70, 300])
+def test_append_finds_the_row_of_every_token(heads, dim, rows):
+    """Runs of unlike lengths, many of them empty, in many rows."""
+    import bucketed_classifier_free_amd as bcg
+    rng = np.random.default_rng(rows)
+    new = [int(n) for n in rng.integers(0, 9, rows) * (rng.random(rows) < 0.6)]
+    new[rng.integers(rows)] += 33
+    c = make_cache(new, heads, dim, 16, "f32", seed=rows, rot=0.0)
+    k = torch.randn((sum(new), heads, dim), device="cuda")
+    want = c["k"].clone()
+    table, off = c["table"].cpu().numpy(), np.concatenate([[0], np.cumsum(new)])
+    for r, n in enumerate(new):
+        for t in range(n):
+            want[table[r, t // 16], :, t % 16] = k[off[r] + t]
+    bcg.cache_append(k, k, c["k"], c["v"], c["table"], c["length"], offset=i32(off.tolist()))
+    torch.cuda.synchronize()
+    assert torch.equal(c["k"], want)
+
+
 def test_append_drops_tokens_without_a_place():
     import bucketed_classifier_free_amd as bcg
     c = make_cache([40, 20, 16], 2, 64, 16, "f32", seed=1, rot=0.0)
@@ -214,7 +234,7 @@ def test_shared_pages_stay_until_their_last_row():
     b.free([3])
 
 
-@pytest.mark.parametrize("rows,length,spare", [(200, 60, 40), (1500, 20, 700), (3, 6000, 5000)])
+@pytest.mark.parametrize("rows,length,spare", [(200, 60, 40), (1500, 20, 700), (3, 6000, 5000), (5000, 30, 9000)])
 def test_many_pages(rows, length, spare):
     rng = np.random.default_rng(rows)
     lens = [int(n) for n in rng.integers(0, length + 1, rows)]
