@@ -21,29 +21,18 @@ namespace {
 
 // Workgroups that a decode launch aims at when it splits the rows' tokens (16
 // a CU: rows of unlike lengths even out), and a prompt launch (2 a CU).
-#ifndef DG
-#define DG 4096
-#endif
-#ifndef NB8
-#define NB8 12
-#endif
-#ifndef LB
-#define LB 64
-#endif
-#ifndef MB
-#define MB 4
-#endif
-constexpr int64_t kDecodeGroups = DG, kPromptGroups = 512;
+constexpr int64_t kDecodeGroups = 4096, kPromptGroups = 512;
 // A split is at least this many blocks (decode: 32 tokens, prompt: 64).
-constexpr int64_t kMinBlocks = MB;
+constexpr int64_t kMinBlocks = 4;
 
-// (query, head) entries of all splits: splits > 1 only while the groups of one
-// split are below the aim, and a group holds at most 16 (decode) or 256
-// (prompt) entries, so splits * entries < aim * group.
+// (query, head) entries of all splits: at most kMaxSplits a query; and splits >
+// 1 only while the groups of one split are below the aim, a group holding at
+// most 16 (decode) or 192 (prompt) entries, so the rest is bounded too (what a
+// launch with few entries a group would want beyond it, it does without).
 int64_t max_parts(int64_t entries) {
-    const int64_t cap = kPromptGroups * 256;
-    static_assert(kPromptGroups * 256 >= kDecodeGroups * 16, "");
-    return entries * kDecodeGroups < cap ? entries * kDecodeGroups : cap;
+    constexpr int64_t cap = kPromptGroups * 256;
+    static_assert(cap >= kDecodeGroups * 16, "");
+    return entries * kMaxSplits < cap ? entries * kMaxSplits : cap;
 }
 
 int check(const bcg_attn_args* a, const char* who, bool prompt) {
@@ -133,10 +122,10 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     int64_t splits = groups >= aim ? 1 : aim / groups;
     if (!prompt) {
         // half of the aim is enough where the splits would get shorter than 64 blocks
-        const int64_t lng = nb / LB > aim / 2 / groups ? nb / LB : aim / 2 / groups;
+        const int64_t lng = nb / 64 > aim / 2 / groups ? nb / 64 : aim / 2 / groups;
         if (splits > lng) splits = lng < 1 ? 1 : lng;
         // short rows: eight waves, and no second launch to join splits
-        if (nb <= NB8 && groups < 1024 && a->q_dtype == BCG_BF16 && a->head_dim <= 128) splits = 1, p.waves = 8;
+        if (nb <= 12 && groups < 1024 && a->q_dtype == BCG_BF16 && a->head_dim <= 128) splits = 1, p.waves = 8;
     }
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits > (nb + least - 1) / least) splits = (nb + least - 1) / least;

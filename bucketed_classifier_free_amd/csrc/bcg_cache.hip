@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p, int s
         }
         row = a;
         pos = p.off[row + 1] - tok;
+        if (pos < 1) return;  // offsets that do not ascend
     }
     pos = min(max(p.len[row], 0), p.maxb * p.ps) - pos;
     if (pos < 0) return;

@@ -213,8 +213,7 @@ extern "C" int guided_logits(const bcg_logits_args* a, void* stream) {
     if (a->logit_stride < a->vocab || a->out_stride < a->vocab)
         return fail(BCG_ESHAPE, "%s: row strides %lld, %lld below the vocabulary's %d", who, (long long)a->logit_stride,
                     (long long)a->out_stride, a->vocab);
-    const bool penal = a->repetition || a->presence || a->frequency || a->prompt_len || a->history_len;
-    if (!a->history && penal) return fail(BCG_EINVAL, "%s: penalties without a history", who);
+    if (!a->history && (a->prompt_len || a->history_len)) return fail(BCG_EINVAL, "%s: lengths without a history", who);
     if (a->history && (!a->history_len || a->max_history < 0)) return fail(BCG_EINVAL, "%s: a history without its lengths", who);
     if (a->history && a->max_history > BCG_MAX_HISTORY)
         return fail(BCG_ESHAPE, "%s: a history of %d tokens (at most %d)", who, a->max_history, BCG_MAX_HISTORY);

@@ -222,10 +222,11 @@ int cache_copy(const bcg_cache* cache, int n, const int32_t* src, const int32_t*
  * is 0.  A sample whose cond_row is outside [0, logit_rows) is not written; an
  * uncond_row beyond it counts as -1.  A masked token is -infinity whatever its
  * logits are; a row whose mask leaves nothing is -infinity throughout.
- * The penalties, bias, temperature and mask are each optional (NULL).
+ * The penalties, bias, temperature and mask are each optional (NULL); without
+ * a history the penalties have nothing to act on.
  * out must not overlap logits (rows of one may serve several samples).
- * Errors: BCG_EINVAL (NULL pointer, penalties without a history, bias without
- * ids, overlap), BCG_ESHAPE, BCG_EDTYPE, BCG_EHIP.
+ * Errors: BCG_EINVAL (NULL pointer, history lengths without a history, bias
+ * without ids, overlap), BCG_ESHAPE, BCG_EDTYPE, BCG_EHIP.
  */
 typedef struct {
     int32_t n, vocab, logit_rows;

@@ -161,7 +161,8 @@ def test_logits_refuse():
             (dict(n=-1), L.BCG_ESHAPE, "n -1"), (dict(n=65536), L.BCG_ESHAPE, "65535"), (dict(vocab=-1), L.BCG_ESHAPE, "vocab"),
             (dict(dtype=2), L.BCG_EDTYPE, "dtype"), (dict(out_dtype=5), L.BCG_EDTYPE, "dtype"), (dict(logits=None), L.BCG_EINVAL, "NULL"),
             (dict(cond_row=None), L.BCG_EINVAL, "NULL"), (dict(scale=None), L.BCG_EINVAL, "scale"), (dict(logit_stride=99), L.BCG_ESHAPE, "strides"),
-            (dict(out_stride=99), L.BCG_ESHAPE, "strides"), (dict(presence=addr(5)), L.BCG_EINVAL, "history"),
+            (dict(out_stride=99), L.BCG_ESHAPE, "strides"), (dict(prompt_len=addr(5)), L.BCG_EINVAL, "history"), (dict(history_len=addr(5)), L.BCG_EINVAL, "history"),
+            (dict(history=addr(5), history_len=addr(6), max_history=1 << 18), L.BCG_ESHAPE, "at most"),
             (dict(history=addr(5), max_history=4), L.BCG_EINVAL, "lengths"), (dict(bias=addr(5)), L.BCG_EINVAL, "bias"),
             (dict(bias=addr(5), bias_ids=addr(6), num_biases=5000), L.BCG_ESHAPE, "biases"), (dict(mask=addr(5), mask_words=3), L.BCG_ESHAPE, "mask"),
             (dict(out=addr(0) + 200), L.BCG_EINVAL, "overlaps")]:

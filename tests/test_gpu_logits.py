@@ -128,6 +128,13 @@ def test_ids_lengths_and_rows_out_of_range():
     assert (got[:2] == 7.0).all()
 
 
+def test_penalties_without_a_history_do_nothing():
+    logits, kw = case(3, 300, "f32", seed=8, hist=5)
+    want = run(logits, {k: v for k, v in kw.items() if k in ("cond_row", "uncond_row", "scale", "temperature")})
+    got = run(logits, {k: v for k, v in kw.items() if k not in ("history", "history_len", "prompt_len")})
+    assert torch.equal(got, want)
+
+
 def test_the_last_bias_of_a_token_counts():
     logits, kw = case(1, 100, "f32", seed=6, guided=False)
     kw["bias_ids"] = np.array([[5, 9, 5, 9, 5]], np.int32)
