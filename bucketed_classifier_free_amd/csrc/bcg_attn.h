@@ -51,8 +51,10 @@ __device__ __forceinline__ BlockList visible_blocks(int lo, int hi, int sinks, i
 
 template <typename QT, typename KT> hipError_t launch_decode(const AttnParams& p, hipStream_t st);
 template <typename QT, typename KT> hipError_t launch_prompt(const AttnParams& p, hipStream_t st);
-// Columns (query, head) of one prompt workgroup, for runs of many queries.
+// Columns (query, head) of one prompt workgroup, for runs of many queries, and
+// tokens of its tiles.
 template <typename QT, typename KT> int prompt_columns(int head_dim);
+template <typename QT, typename KT> int prompt_block(int head_dim);
 
 struct e4m3_t { uint8_t b; };
 

@@ -16,13 +16,16 @@ extern template hipError_t launch_prompt<float, float>(const AttnParams&, hipStr
 extern template int prompt_columns<bf16_t, bf16_t>(int);
 extern template int prompt_columns<bf16_t, e4m3_t>(int);
 extern template int prompt_columns<float, float>(int);
+extern template int prompt_block<bf16_t, bf16_t>(int);
+extern template int prompt_block<bf16_t, e4m3_t>(int);
+extern template int prompt_block<float, float>(int);
 
 namespace {
 
 // Workgroups that a decode launch aims at when it splits the rows' tokens (16
 // a CU: rows of unlike lengths even out), and a prompt launch (2 a CU).
 constexpr int64_t kDecodeGroups = 4096, kPromptGroups = 512;
-// A split is at least this many blocks (decode: 32 tokens, prompt: 64).
+// A split is at least this many blocks (decode: 32 tokens, prompt: 32 or 64).
 constexpr int64_t kMinBlocks = 4;
 
 // (query, head) entries of all splits: at most kMaxSplits a query; and splits >
@@ -96,13 +99,13 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     p.window = a->window; p.sinks = a->window > 0 ? a->sinks : 0; p.max_len = a->max_len;
     p.max_new = a->max_new;
     p.scale2 = a->scale * 1.4426950408889634f;
-    const int T = prompt ? 64 : 32;  // tokens of a block
-    int C = 16;                      // columns of a workgroup
+    int T = 32, C = 16;  // tokens of a block, columns of a workgroup
     const int64_t cols = prompt ? (int64_t)a->max_new * p.G : p.G;
     if (prompt) {
         const int D = a->head_dim;
-        C = a->q_dtype == BCG_F32 ? prompt_columns<float, float>(D)
-            : a->kv_dtype == BCG_BF16 ? prompt_columns<bf16_t, bf16_t>(D) : prompt_columns<bf16_t, e4m3_t>(D);
+        if (a->q_dtype == BCG_F32) T = prompt_block<float, float>(D), C = prompt_columns<float, float>(D);
+        else if (a->kv_dtype == BCG_BF16) T = prompt_block<bf16_t, bf16_t>(D), C = prompt_columns<bf16_t, bf16_t>(D);
+        else T = prompt_block<bf16_t, e4m3_t>(D), C = prompt_columns<bf16_t, e4m3_t>(D);
         if (cols <= 64) C = 64;
     }
     p.columns = C;

@@ -5,4 +5,5 @@ namespace bcg {
 template hipError_t launch_decode<bf16_t, e4m3_t>(const AttnParams&, hipStream_t);
 template hipError_t launch_prompt<bf16_t, e4m3_t>(const AttnParams&, hipStream_t);
 template int prompt_columns<bf16_t, e4m3_t>(int);
+template int prompt_block<bf16_t, e4m3_t>(int);
 }  // namespace bcg

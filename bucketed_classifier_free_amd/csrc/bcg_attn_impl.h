@@ -504,13 +504,18 @@ template <typename QT, int DP, int TT> struct Tile {
 // products.  In fp32 a product takes 16 times as long and one tile is enough.
 template <typename QT, int DP> constexpr int prompt_r() { return sizeof(QT) == 4 || DP == 256 ? 1 : DP == 128 ? 2 : 3; }
 
+// Tokens of a tile: 64, or 32 where this lets two workgroups' tiles fit a CU's
+// LDS (bf16 of 256: 405 -> 736 TF/s over 8192 tokens, fp32 of 128: 78 -> 106
+// over 2048).  fp32 of 256 has one workgroup either way, and one buffer.
+template <typename QT, int DP> constexpr int prompt_t() { return DP * (int)sizeof(QT) == 512 ? 32 : 64; }
+
 // One workgroup: 64 * R columns (query, head of the kv head's group) of one
-// row, four waves of R 16-column tiles each, against 64-token tiles of keys
+// row, four waves of R 16-column tiles each, against tiles of tokens of keys
 // and values in LDS.  Each wave stages 16 tokens (one page) of the next tile
 // while all compute on the present one; one barrier a tile.
 template <typename QT, typename KT, int DP, int R, bool EX>
 __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
-    typedef Tile<QT, DP, 64> L;
+    typedef Tile<QT, DP, prompt_t<QT, DP>()> L;
     constexpr int E = L::E, S = L::S, T = L::T, C = 64 * R, CH = L::CH;
     constexpr int NB = L::kBytes <= 32768 ? 2 : 1;  // two tiles in flight while LDS holds them
     constexpr int KB = T / 32, WT = T / 4, NP = T / 16, NL = WT * CH / 64;  // a wave stages WT tokens in NL loads a side
@@ -962,6 +967,9 @@ template <typename QT, typename KT> hipError_t launch_decode(const AttnParams& p
 }
 template <typename QT, typename KT> int prompt_columns(int D) {
     return 64 * (D <= 64 ? attn::prompt_r<QT, 64>() : D <= 128 ? attn::prompt_r<QT, 128>() : attn::prompt_r<QT, 256>());
+}
+template <typename QT, typename KT> int prompt_block(int D) {
+    return D <= 64 ? attn::prompt_t<QT, 64>() : D <= 128 ? attn::prompt_t<QT, 128>() : attn::prompt_t<QT, 256>();
 }
 template <typename QT, typename KT> hipError_t launch_prompt(const AttnParams& p, hipStream_t st) {
     if (p.D <= 64) return attn::prompt_dp<QT, KT, 64>(p, st);
