@@ -320,18 +320,21 @@ __global__ void __launch_bounds__(64 * NW) decode_kernel(const AttnParams p) {
     const KT* vc = static_cast<const KT*>(p.v) + (int64_t)h * p.ps * p.D;
 
     // Table entries are read 32 blocks at a time, one 16-token part a lane, and
-    // a group ahead: a block's pages are then two reads of a lane.
-    int part_page = -1, part_in = 0, next_page = -1, next_in = 0;
+    // a group ahead: a block's pages are then two reads of a lane.  Without a
+    // window the first group does not wait for the row's length.
+    int part_page = -1, part_in = 0, next_page = -1, next_t = 0;
     auto read_group = [&](int vb) {
-        const int v = vb + (lane >> 1) * NW, t = bl(v) * 32 + (lane & 1) * 16;
-        next_page = v < v1 && t < len ? table[p.shift >= 0 ? t >> p.shift : t / p.ps] : -1;
-        next_in = p.shift >= 0 ? t & (p.ps - 1) : t % p.ps;
+        const int v = vb + (lane >> 1) * NW;
+        next_t = (p.window > 0 ? bl(v) : v) * 32 + (lane & 1) * 16;
+        next_page = -1;
+        if (v < v0 + p.chunk && next_t < (p.window > 0 ? len : p.max_len))
+            next_page = table[p.shift >= 0 ? next_t >> p.shift : next_t / p.ps];
     };
-    if (v0 + wave < v1) read_group(v0 + wave);
+    read_group(v0 + wave);
     for (int vb = v0 + wave, n = 0; vb < v1; vb += NW, ++n) {
         if ((n & 31) == 0) {
-            part_page = next_page < p.np ? next_page : -1;
-            part_in = next_in;
+            part_page = next_t < len && next_page < p.np ? next_page : -1;
+            part_in = p.shift >= 0 ? next_t & (p.ps - 1) : next_t % p.ps;
             if (vb + 32 * NW < v1) read_group(vb + 32 * NW);
         }
         const int t0 = bl(vb) * 32;
@@ -529,8 +532,12 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
     unsigned id = blockIdx.x;
     const int h = id % p.kvh; id /= p.kvh;
     const int split = id % p.splits; id /= p.splits;
-    const int row = id % p.rows;
-    const int tile = p.tiles - 1 - (int)(id / p.rows);  // the longest first
+    // The longest tiles first, and each row in turn at every place: workgroups
+    // are dealt out to the shader engines in turn, and rows at a fixed place of
+    // eight leave the engine of the longest row busy alone (prompt_batch of the
+    // measured cases: 264 us; with the rows turned on from tile to tile 224).
+    const int tile = p.tiles - 1 - (int)(id / p.rows);
+    const int row = (int)((id + id / p.rows) % p.rows);
     const int q0 = min(max(p.qoff[row], 0), p.tokens);
     const int n = min(max(p.qoff[row + 1], q0), p.tokens) - q0;
     const int cols = min(n, p.max_new) * p.G, c0 = tile * C;

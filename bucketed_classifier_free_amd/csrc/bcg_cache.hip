@@ -63,18 +63,21 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p, int s
     };
     int c0 = (int)id & (lanes - 1);
     get(c0);  // on their way while the token's place is found
-    int row = tok, pos = 1;
-    if (p.off) {
+    int row = tok, pos = 1, len = 0;
+    if (!p.off) {
+        len = p.len[row];
+    } else {
         // the row whose run holds the token: the last one that begins at or before it
         int a = 0, b = p.rows;  // off[a] <= tok < off[b]
         const int g = min((int)((int64_t)tok * p.rows / p.tokens), p.rows - 1);  // runs of like lengths: at once
-        const int first = p.off[0], end = p.off[p.rows], at = p.off[g], next = p.off[g + 1];
+        const int first = p.off[0], end = p.off[p.rows], at = p.off[g], next = p.off[g + 1], guess = p.len[g];
         if (first > tok || end <= tok) return;
-        if (at <= tok && tok < next) {
+        const bool found = at <= tok && tok < next;
+        if (found) {
             a = g;
-            b = g + 1;
-        }
-        if (shift == 6) {
+            pos = next - tok;
+            len = guess;
+        } else if (shift == 6) {
             // a wave's token: 64 places of the range at a time
             const int lane = (int)id & 63;
             while (b - a > 1) {
@@ -91,10 +94,13 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p, int s
             }
         }
         row = a;
-        pos = p.off[row + 1] - tok;
-        if (pos < 1) return;  // offsets that do not ascend
+        if (!found) {
+            pos = p.off[a + 1] - tok;
+            len = p.len[a];
+            if (pos < 1) return;  // offsets that do not ascend
+        }
     }
-    pos = min(max(p.len[row], 0), p.maxb * p.ps) - pos;
+    pos = min(max(len, 0), p.maxb * p.ps) - pos;
     if (pos < 0) return;
     const int blk = pos / p.ps, pg = p.table[(int64_t)row * p.maxb + blk];
     if (pg < 0 || pg >= p.np) return;
