@@ -228,7 +228,9 @@ __device__ __forceinline__ void store_row(QT* out, const float (&x)[E], int d, i
 
 // One wave a (token, head): out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
 // Lane s holds the weight of split s (and s + 64); the splits' rows are then
-// read 64 / LR at a time (LR lanes of four dimensions a row), four loads in flight.
+// read 64 / LR at a time (LR lanes of four dimensions a row), four loads in
+// flight.  64 splits of 4 rows of 64 heads: 10.6 us (one split after the other,
+// each waiting for its weight: 44 us more on the whole call).
 template <typename QT, int DP> __device__ __forceinline__ void join_splits(const AttnParams& p, int64_t at) {
     constexpr int LR = DP / 4, NG = 64 / LR;
     const int64_t n = (int64_t)p.tokens * p.qh;
@@ -285,7 +287,17 @@ template <typename QT, int DP> __device__ __forceinline__ void join_splits(const
 // One workgroup: the tokens of one split of a row for up to 16 query heads of
 // one kv head.  NW waves take the split's 32-token blocks in turn, straight
 // from memory into registers (each key and value is used once, so there is
-// nothing for LDS to share); their states are joined in LDS at the end.
+// nothing for LDS to share; three waves a SIMD with 16 KB of loads each keep
+// more in flight than the memory needs); their states are joined in LDS at the
+// end.  Bound by HBM: 4 rows of up to 131072 tokens (64 query heads over 8 of
+// 128, bf16, 2.0 GB) 350 us = 5.7 TB/s, where a 2 GiB device copy moves 4.9;
+// 96 rows of up to 8192 in e4m3 (0.72 GB) 145 us = 5.0 TB/s.  One short row
+// (700 tokens, two rows) is a chain of loads (length, table, pages): 6.1 us, and
+// 3.7 us for the join.  Joining in the same launch, by the last workgroup of a
+// row, was slower: with fences 866 us instead of 150 (each writes back and drops
+// an L2 that the pages stream through), with device-scope accesses 180.  Eight
+// waves without a second launch pay up to 12 blocks (300 tokens: 8.1 us instead
+// of 12.7 with the join; 700 tokens: 11.3 instead of 9.0).
 template <typename QT, typename KT, int DP, int NW, bool EX>
 __global__ void __launch_bounds__(64 * NW) decode_kernel(const AttnParams p) {
     constexpr int E = DP / 16, S = DP / 32;
@@ -514,8 +526,24 @@ template <typename QT, int DP> constexpr int prompt_t() { return DP * (int)sizeo
 
 // One workgroup: 64 * R columns (query, head of the kv head's group) of one
 // row, four waves of R 16-column tiles each, against tiles of tokens of keys
-// and values in LDS.  Each wave stages 16 tokens (one page) of the next tile
-// while all compute on the present one; one barrier a tile.
+// and values in LDS.  Each wave stages its part of the next tile (a part of one
+// page, by direct loads that pass no register; e4m3 is widened on the way)
+// while all compute on the present one; one barrier a tile.  Keys are read as
+// operands as they lie, bf16 values through transposed LDS reads.
+//
+// What bounds it: the matrix cores and the vector units in turn.  A 64-token
+// tile costs a wave 64 products of 16 cycles and about 200 vector instructions,
+// 32 of them exponentials at a quarter of the rate; two waves a SIMD overlap
+// the two in part.  16384 tokens, 32/8 heads of 128, bf16, causal: 2.2 ms = 1.0
+// PF/s, where a bf16 matrix product of 8192 reaches 1.18.  Eight ragged prompts
+// of 830 to 2048: 224 us = 751 TF/s; 8192 tokens in a window of 1024 with 4
+// sinks: 174 us = 741 TF/s.  Shorter runs lose to the partly seen tiles, to the
+// reads of the queries and the stores of the outputs (50 of the 224 us without
+// any tile) and to each workgroup's first loads.  Tried, on the eight prompts:
+// R = 1 408 us, R = 3 484 and R = 4 1019 (registers spill), eight waves on the
+// same tile 296 instead of 270, 32-token tiles 296 instead of 274 (318 with three
+// waves a SIMD), products and vector work interleaved by scheduling groups 286
+// instead of 279, wave priorities around the products 282.
 template <typename QT, typename KT, int DP, int R, bool EX>
 __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
     typedef Tile<QT, DP, prompt_t<QT, DP>()> L;
@@ -534,8 +562,8 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
     const int split = id % p.splits; id /= p.splits;
     // The longest tiles first, and each row in turn at every place: workgroups
     // are dealt out to the shader engines in turn, and rows at a fixed place of
-    // eight leave the engine of the longest row busy alone (prompt_batch of the
-    // measured cases: 264 us; with the rows turned on from tile to tile 224).
+    // eight leave the engine of the longest row busy alone (eight ragged prompts:
+    // 264 us; with the rows turned on from tile to tile 224).
     const int tile = p.tiles - 1 - (int)(id / p.rows);
     const int row = (int)((id + id / p.rows) % p.rows);
     const int q0 = min(max(p.qoff[row], 0), p.tokens);

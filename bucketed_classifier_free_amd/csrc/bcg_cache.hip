@@ -42,7 +42,11 @@ __device__ __forceinline__ float clamp448(float x) { return x != x ? x : fminf(f
 template <typename QT> struct Chunk { u32x4_t w[sizeof(QT) / 2]; };
 
 // `lanes` lanes (a power of two) a token, each every lanes-th chunk of its key
-// and its value, two of each in flight.
+// and its value, two of each in flight; a token's place is found once for all
+// of them.  HBM-bound: 13.2 thousand tokens of 8 heads of 128 in bf16 (108 MB)
+// 18.2 us = 5.9 TB/s into pages that the last-level cache partly holds, 25 us
+// in turn with others; with one 16-byte chunk a lane, each finding its token's
+// place alone, 39.  One token for each of 96 rows is a chain of loads: 5.2 us.
 template <typename QT, bool E4M3>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p, int shift) {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -376,7 +380,8 @@ template <int NT> __global__ void __launch_bounds__(NT) fork_kernel(const CacheP
 }
 
 // After fork_kernel: blocks [0, n) copy fork i's table row; the others copy
-// the partly filled pages, one (fork, plane, part) at a time.
+// the partly filled pages, one (fork, plane, part) at a time.  (8 forks of a
+// 64-row batch: 5.2 us for the bookkeeping, 3.8 for this.)
 __device__ __forceinline__ void copy_page(const CacheParams& p, int plane, int from, int to, int v0, int v1) {
     const u32x4_t* a = reinterpret_cast<const u32x4_t*>(p.pool + plane * p.plane + from * p.page);
     u32x4_t* b = reinterpret_cast<u32x4_t*>(p.pool + plane * p.plane + to * p.page);
@@ -446,7 +451,8 @@ __global__ void __launch_bounds__(256) free_kernel(const CacheParams p, const in
 // ---------------------------------------------------------------- compact
 
 // The moves: fresh[p] = new place of page p; pair[2k], pair[2k + 1] = from, to
-// of move k; owner[0] = their count (rows >= 1) -- kept in pair's last word.
+// of move k; owner[0] = their count.  (2700 pages: 8.6 us, a tenth of the copies
+// that follow: 685 MB in 140 us = 4.9 TB/s, what a plain device copy reaches.)
 template <int NT> __global__ void __launch_bounds__(NT) compact_plan_kernel(const CacheParams p, int32_t* refs_out, int32_t* moved) {
     __shared__ int ws[NT / 64];
     __shared__ int64_t ws64[NT / 64];
