@@ -25,8 +25,9 @@ namespace {
 // Workgroups that a decode launch aims at when it splits the rows' tokens (16
 // a CU: rows of unlike lengths even out), and a prompt launch (2 a CU).
 constexpr int64_t kDecodeGroups = 4096, kPromptGroups = 512;
-// A split is at least this many blocks (decode: 32 tokens, prompt: 32 or 64).
-constexpr int64_t kMinBlocks = 4;
+// A split is at least this many blocks (decode: 32 tokens; prompt: 32 or 64, and
+// half as many in fp32): shorter ones cost more to join than they save.
+constexpr int64_t kMinBlocks = 4, kMinTiles = 8;
 
 // (query, head) entries of all splits: at most kMaxSplits a query; and splits >
 // 1 only while the groups of one split are below the aim, a group holding at
@@ -106,7 +107,10 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
         if (a->q_dtype == BCG_F32) T = prompt_block<float, float>(D), C = prompt_columns<float, float>(D);
         else if (a->kv_dtype == BCG_BF16) T = prompt_block<bf16_t, bf16_t>(D), C = prompt_columns<bf16_t, bf16_t>(D);
         else T = prompt_block<bf16_t, e4m3_t>(D), C = prompt_columns<bf16_t, e4m3_t>(D);
-        if (cols <= 64) C = 64;
+        // narrow workgroups where the wide ones would not be two a CU: each tile
+        // is done sooner, and nobody waits for the CUs (512 tokens, 32/8 heads of
+        // 128: 26.4 -> 14.9 us; 20 rows of 30 new over 300: 23.9 -> 15.0)
+        if (cols <= 64 || ((a->tokens * (int64_t)p.G + C - 1) / C + a->rows) * p.kvh < kPromptGroups) C = 64;
     }
     p.columns = C;
     p.tiles = (int)((cols + C - 1) / C);
@@ -121,7 +125,7 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     const int64_t groups = (int64_t)(prompt ? (a->tokens * (int64_t)p.G + C - 1) / C + a->rows : (int64_t)a->rows * p.tiles) * p.kvh;
     // (in fp32 a prompt's tile takes several times as long: twice as many splits)
     const bool slow = prompt && a->q_dtype == BCG_F32;
-    const int64_t aim = !prompt ? kDecodeGroups : slow ? 2 * kPromptGroups : kPromptGroups, least = slow ? kMinBlocks / 2 : kMinBlocks;
+    const int64_t aim = !prompt ? kDecodeGroups : slow ? 2 * kPromptGroups : kPromptGroups, least = !prompt ? kMinBlocks : slow ? kMinTiles / 2 : kMinTiles;
     int64_t splits = groups >= aim ? 1 : aim / groups;
     if (!prompt) {
         // half of the aim is enough where the splits would get shorter than 64 blocks

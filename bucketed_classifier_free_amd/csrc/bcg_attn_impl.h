@@ -564,6 +564,10 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
     // are dealt out to the shader engines in turn, and rows at a fixed place of
     // eight leave the engine of the longest row busy alone (eight ragged prompts:
     // 264 us; with the rows turned on from tile to tile 224).
+    // A grid of at most two workgroups a CU: the second ones the shortest first,
+    // so that a long one shares its CU with a short one.
+    const int inner = p.kvh * p.splits, all = p.rows * p.tiles, once = 256 / inner;
+    if ((int64_t)all * inner <= 512 && (int)id >= once) id = all - 1 - ((int)id - once);
     const int tile = p.tiles - 1 - (int)(id / p.rows);
     const int row = (int)((id + id / p.rows) % p.rows);
     const int q0 = min(max(p.qoff[row], 0), p.tokens);
