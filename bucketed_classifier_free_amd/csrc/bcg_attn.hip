@@ -84,6 +84,29 @@ int check(const bcg_attn_args* a, const char* who, bool prompt) {
     return BCG_OK;
 }
 
+// A decode's rows whole, without a second launch that joins splits: where the
+// workgroups fill the card with up to eight waves each (four for heads above
+// 128, whose outputs fill LDS), as long as a wave has no more than 16 blocks (in
+// fp32, whose blocks take longer, twice the waves and 4 blocks); and short rows
+// always.  No more waves than fill the card, nor than the blocks of a row: a
+// wave alone has nobody to join in LDS.  32/8 heads of 128 in bf16, rows of up to
+//   20 tokens, 128 rows: 12.0 us in workgroups of eight, 7.2 of one wave
+//   250 tokens, 128 rows: 25.6 split in two, 16.9 of two waves
+//   500 tokens, 64 rows: 23.7 split, 16.8 of four;  32 rows: 17.3, 12.7 of eight
+//   2000 tokens, 32 rows: 34.9 split, 34.1 of eight;  16 rows of 500: 13.5, 11.8
+// and where it ends
+//   1500 tokens, 256 rows in e4m3: 83.0 split, 94.1 of one wave
+//   2000 tokens, 32 rows in fp32: 79.8 split, 87.4 of eight
+bool one_launch(const bcg_attn_args* a, int64_t groups, int64_t nb, int* waves) {
+    const bool f32 = a->q_dtype == BCG_F32;
+    const int most = a->head_dim <= 128 ? 8 : 4;
+    const bool brief = nb <= kMinBlocks || (nb <= 12 && !f32 && a->head_dim <= 128);
+    int w = nb <= (f32 ? 1 : 2) ? 1 : nb <= 8 && !(f32 && nb > kMinBlocks) ? 4 : most;
+    while (w > 1 && groups * w > 2048) w /= 2;
+    *waves = w;
+    return brief || (groups * most >= (f32 ? 2048 : 1024) && nb <= (f32 ? 4 : 16) * w && (nb <= 8 || groups * w <= 2048));
+}
+
 int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     clear_error();
     const int rc = check(a, who, prompt);
@@ -123,16 +146,22 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     }
     nb = nb < 1 ? 1 : nb;
     const int64_t groups = (int64_t)(prompt ? (a->tokens * (int64_t)p.G + C - 1) / C + a->rows : (int64_t)a->rows * p.tiles) * p.kvh;
+    const bool f32 = a->q_dtype == BCG_F32;
+    int64_t aim = kDecodeGroups, least = kMinBlocks;
     // (in fp32 a prompt's tile takes several times as long: twice as many splits)
-    const bool slow = prompt && a->q_dtype == BCG_F32;
-    const int64_t aim = !prompt ? kDecodeGroups : slow ? 2 * kPromptGroups : kPromptGroups, least = !prompt ? kMinBlocks : slow ? kMinTiles / 2 : kMinTiles;
+    if (prompt) aim = f32 ? 2 * kPromptGroups : kPromptGroups, least = f32 ? kMinTiles / 2 : kMinTiles;
     int64_t splits = groups >= aim ? 1 : aim / groups;
     if (!prompt) {
         // half of the aim is enough where the splits would get shorter than 64 blocks
         const int64_t lng = nb / 64 > aim / 2 / groups ? nb / 64 : aim / 2 / groups;
         if (splits > lng) splits = lng < 1 ? 1 : lng;
-        // short rows: eight waves, and no second launch to join splits
-        if (nb <= 12 && groups < 1024 && a->q_dtype == BCG_BF16 && a->head_dim <= 128) splits = 1, p.waves = 8;
+        // and two workgroups a CU where they would get shorter than 16 (8 rows of 4000: 24.7 us,
+        // 20.8 with splits of 15 blocks; one of 16000: 21.6, 19.5 with 8)
+        const int64_t few = groups * nb / 512;
+        least = few < least ? least : few < 16 ? few : 16;
+        p.waves = 4;
+        int waves = 0;
+        if (one_launch(a, groups, nb, &waves)) splits = 1, p.waves = waves;
     }
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits > (nb + least - 1) / least) splits = (nb + least - 1) / least;

@@ -227,18 +227,31 @@ __device__ __forceinline__ void store_row(QT* out, const float (&x)[E], int d, i
 // ---------------------------------------------------------------- join
 
 // One wave a (token, head): out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
-// Lane s holds the weight of split s (and s + 64); the splits' rows are then
-// read 64 / LR at a time (LR lanes of four dimensions a row), four loads in
-// flight.  64 splits of 4 rows of 64 heads: 10.6 us (one split after the other,
-// each waiting for its weight: 44 us more on the whole call).
-template <typename QT, int DP> __device__ __forceinline__ void join_splits(const AttnParams& p, int64_t at) {
-    constexpr int LR = DP / 4, NG = 64 / LR;
+// Lane s holds the weight of split s (and s + 64); the splits' rows are read
+// 64 / LR at a time (LR lanes of four dimensions a row), four loads in flight,
+// the first four before the weights are known (what no split wrote counts for
+// nothing).  More splits than that are shared by NW = 4 waves, joined in LDS:
+// one row of 8000 tokens (63 splits of 32 heads) 19.2 -> 15.4 us, call and join.
+template <typename QT, int DP, int NW> __device__ __forceinline__ void join_splits(const AttnParams& p, int64_t at) {
+    constexpr int LR = DP / 4, NG = 64 / LR, U = 4;
     const int64_t n = (int64_t)p.tokens * p.qh;
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, wave = NW > 1 ? threadIdx.x >> 6 : 0;
+    const int d = lane % LR * 4, sub = lane / LR;
+    const float* po = p.part_o + at * p.D + (d < p.D ? d : 0);
     float2 ml[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         ml[k] = lane + 64 * k < p.splits ? p.part_ml[(lane + 64 * k) * n + at] : make_float2(kNegInf, 0.0f);
+    f32x4_t y[U];
+    auto read = [&](int s0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * NG + sub;
+            y[u] = f32x4_t{0, 0, 0, 0};
+            if (s < p.splits) y[u] = *reinterpret_cast<const f32x4_t*>(po + s * n * p.D);
+        }
+    };
+    read(wave * U * NG);
     float top = fmaxf(ml[0].x, ml[1].x);
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
@@ -252,31 +265,36 @@ template <typename QT, int DP> __device__ __forceinline__ void join_splits(const
     }
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k);
-    const int d = lane % LR * 4, sub = lane / LR;
     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float* po = p.part_o + at * p.D + (d < p.D ? d : 0);
-    for (int s0 = 0; s0 < p.splits; s0 += 4 * NG) {
-        f32x4_t y[4];
-        float f[4];
+    for (int s0 = wave * U * NG; s0 < p.splits; s0 += NW * U * NG) {
+        if (s0 >= NW * U * NG) read(s0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int s = s0 + u * NG + sub;
             const float fa = __shfl(w[0], s & 63), fb = __shfl(w[1], s & 63);
-            f[u] = s < p.splits ? (s < 64 ? fa : fb) : 0.0f;
-            y[u] = f32x4_t{0, 0, 0, 0};
-            if (f[u] != 0.0f) y[u] = *reinterpret_cast<const f32x4_t*>(po + s * n * p.D);
+            const float f = s < p.splits ? (s < 64 ? fa : fb) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] += f == 0.0f ? 0.0f : f * y[u][i];
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] += f[u] * y[u][i];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int k = LR; k < 64; k <<= 1) x[i] += __shfl_xor(x[i], k);
-        x[i] = sum == 0.0f ? 0.0f : x[i] / sum;
+    if constexpr (NW > 1) {
+        __shared__ __attribute__((aligned(16))) float x_s[NW][DP];
+        if (sub == 0) *reinterpret_cast<f32x4_t*>(x_s[wave] + d) = f32x4_t{x[0], x[1], x[2], x[3]};
+        __syncthreads();
+        if (wave) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NW; ++v) x[i] += x_s[v][d + i];
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = sum == 0.0f ? 0.0f : x[i] / sum;
     if (sub == 0) store_row<QT, 4>(static_cast<QT*>(p.out) + at * p.D, x, d, p.D);
     if (p.lse && lane == 0)
         p.lse[at] = sum == 0.0f ? kNegInf : (top == kNegInf ? sum : (top + __log2f(sum)) * 0.69314718055994531f);
@@ -295,15 +313,12 @@ template <typename QT, int DP> __device__ __forceinline__ void join_splits(const
 // (700 tokens, two rows) is a chain of loads (length, table, pages): 6.1 us, and
 // 3.7 us for the join.  Joining in the same launch, by the last workgroup of a
 // row, was slower: with fences 866 us instead of 150 (each writes back and drops
-// an L2 that the pages stream through), with device-scope accesses 180.  Eight
-// waves without a second launch pay up to 12 blocks (300 tokens: 8.1 us instead
-// of 12.7 with the join; 700 tokens: 11.3 instead of 9.0).
+// an L2 that the pages stream through), with device-scope accesses 180.  Heads
+// of 256 in registers for two waves a SIMD: 16 rows of 2000 tokens 67 -> 47 us.
 template <typename QT, typename KT, int DP, int NW, bool EX>
-__global__ void __launch_bounds__(64 * NW) decode_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(64 * NW, sizeof(QT) == 2 && (EX || sizeof(KT) == 1) && DP == 256 && NW <= 4 ? 2 : 1) decode_kernel(const AttnParams p) {
     constexpr int E = DP / 16, S = DP / 32;
     typedef typename Op<QT>::F8 F8;
-    __shared__ float2 ml_s[NW][16];
-    __shared__ __attribute__((aligned(16))) float o_s[NW][16][DP];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     unsigned id = blockIdx.x;
@@ -409,8 +424,25 @@ __global__ void __launch_bounds__(64 * NW) decode_kernel(const AttnParams p) {
         for (int j = 0; j < E; ++j) Op<QT>::mma(v_frag<QT, KT, E>(v, j), pf, o[j]);
     }
 
-    // join the waves
     l = col_sum(l);
+    if constexpr (NW == 1) {
+        // a wave alone has its columns' outputs in its registers, 4 E dimensions a lane, and its rows are whole
+        if (c >= nh) return;
+        const int64_t at = (int64_t)row * p.qh + head0 + c;
+        const float inv = l == 0.0f ? 0.0f : (p.vscale ? p.vscale[h] : 1.0f) / l;
+        float x[4 * E];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < E; ++j) x[i * E + j] = o[j][i] * inv;
+        store_row<QT, 4 * E>(static_cast<QT*>(p.out) + at * p.D, x, g * 4 * E, p.D);
+        if (p.lse && g == 0) p.lse[at] = l == 0.0f ? kNegInf : (m == kNegInf ? l : (m + __log2f(l)) * 0.69314718055994531f);
+        return;
+    }
+
+    // join the waves
+    __shared__ float2 ml_s[NW][16];
+    __shared__ __attribute__((aligned(16))) float o_s[NW][16][DP];
     if (g == 0) ml_s[wave][c] = make_float2(m, l);
     __syncthreads();
     {
@@ -946,8 +978,8 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const AttnParams p) {
 }
 
 
-template <typename QT, int DP> __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
-    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+template <typename QT, int DP, int NW> __global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
+    const int64_t at = NW > 1 ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (at >= (int64_t)p.tokens * p.qh) return;
     if (p.qoff) {
@@ -960,25 +992,28 @@ template <typename QT, int DP> __global__ void __launch_bounds__(256) join_kerne
         }
         if (!__any(mine)) return;
     }
-    join_splits<QT, DP>(p, at);
+    join_splits<QT, DP, NW>(p, at);
 }
 
 template <typename QT, int DP> inline hipError_t launch_join(const AttnParams& p, hipStream_t st) {
     const int64_t n = (int64_t)p.tokens * p.qh;
-    hipLaunchKernelGGL((join_kernel<QT, DP>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, p);
+    // (n * splits is within max_parts' bound)
+    if (p.splits > 1024 / DP) hipLaunchKernelGGL((join_kernel<QT, DP, 4>), dim3((unsigned)n), dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((join_kernel<QT, DP, 1>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 
+template <typename QT, typename KT, int DP, int NW> inline void decode_launch(const AttnParams& p, hipStream_t st) {
+    const dim3 grid((unsigned)((int64_t)p.rows * p.splits * p.kvh * p.tiles));
+    if (p.D == DP) hipLaunchKernelGGL((decode_kernel<QT, KT, DP, NW, true>), grid, dim3(64 * NW), 0, st, p);
+    else hipLaunchKernelGGL((decode_kernel<QT, KT, DP, NW, false>), grid, dim3(64 * NW), 0, st, p);
+}
 template <typename QT, typename KT, int DP>
 inline hipError_t decode_dp(const AttnParams& p, hipStream_t st) {
-    const dim3 grid((unsigned)((int64_t)p.rows * p.splits * p.kvh * p.tiles));
-    if (p.waves == 8) {
-        if (p.D == DP) hipLaunchKernelGGL((decode_kernel<QT, KT, DP, 8, true>), grid, dim3(512), 0, st, p);
-        else hipLaunchKernelGGL((decode_kernel<QT, KT, DP, 8, false>), grid, dim3(512), 0, st, p);
-    } else {
-        if (p.D == DP) hipLaunchKernelGGL((decode_kernel<QT, KT, DP, 4, true>), grid, dim3(256), 0, st, p);
-        else hipLaunchKernelGGL((decode_kernel<QT, KT, DP, 4, false>), grid, dim3(256), 0, st, p);
-    }
+    if (p.waves == 1) decode_launch<QT, KT, DP, 1>(p, st);
+    else if (p.waves == 2) decode_launch<QT, KT, DP, 2>(p, st);
+    else if (DP > 128 || p.waves == 4) decode_launch<QT, KT, DP, 4>(p, st);
+    else decode_launch<QT, KT, (DP > 128 ? 128 : DP), 8>(p, st);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || p.splits == 1 ? e : launch_join<QT, DP>(p, st);
 }

@@ -344,6 +344,32 @@ def test_decode_many_rows_without_splits(q, kv):
     check(*decode(c, x), ref, dim, n, TYPES[q])
 
 
+@pytest.mark.parametrize("q,kv", KINDS)
+@pytest.mark.parametrize("dim,page", [(48, 16), (64, 32), (128, 16), (208, 48), (256, 16)])
+@pytest.mark.parametrize("rows,top,window,sinks", [(3, 64, 0, 0), (40, 90, 0, 0), (40, 300, 20, 3), (100, 250, 0, 0), (190, 130, 0, 0)])
+def test_decode_rows_whole_in_one_launch(q, kv, dim, page, rows, top, window, sinks):
+    """Rows that are not split, over workgroups of one, two, four and eight waves."""
+    kv_heads = 8
+    lens = [top if i == 0 else (i * 37) % (top + 1) for i in range(rows)]
+    c = make_cache(lens, kv_heads, dim, page, kv, seed=rows + dim)
+    x = make_queries(rows, 16, dim, q, seed=rows)
+    out, lse = decode(c, x, window, sinks)
+    check(out, lse, reference(x, np.arange(rows + 1), c, dim ** -0.5, window, sinks), dim, top, TYPES[q])
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[40, 700], [0, 2100, 1], [4500, 33]])
+def test_decode_few_and_many_splits_are_joined(q, kv, dim, lens):
+    """Up to 64 splits, most of them empty for the short rows."""
+    import bucketed_classifier_free_amd as bcg
+    c = make_cache(lens, 2, dim, 32, kv, seed=dim)
+    x = make_queries(len(lens), 6, dim, q, seed=dim)
+    ws = torch.full_like(bcg.attention_workspace(*x.shape), 255)  # NaN throughout
+    out, lse = decode(c, x, workspace=ws)
+    check(out, lse, reference(x, np.arange(len(lens) + 1), c, dim ** -0.5, 0, 0), dim, max(lens), TYPES[q])
+
+
 def test_decode_many_short_rows():
     rng = np.random.default_rng(1)
     lens = [int(n) for n in rng.integers(0, 50, 600)]
