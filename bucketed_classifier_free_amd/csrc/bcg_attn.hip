@@ -25,9 +25,9 @@ namespace {
 // Workgroups that a decode launch aims at when it splits the rows' tokens (16
 // a CU: rows of unlike lengths even out), and a prompt launch (2 a CU).
 constexpr int64_t kDecodeGroups = 4096, kPromptGroups = 512;
-// A split is at least this many blocks (decode: 32 tokens; prompt: 32 or 64, and
-// half as many in fp32): shorter ones cost more to join than they save.
-constexpr int64_t kMinBlocks = 4, kMinTiles = 8;
+// A decode's split is at least this many blocks of 32 tokens: shorter ones cost
+// more to join than they save.
+constexpr int64_t kMinBlocks = 4;
 
 // (query, head) entries of all splits: at most kMaxSplits a query; and splits >
 // 1 only while the groups of one split are below the aim, a group holding at
@@ -107,6 +107,31 @@ bool one_launch(const bcg_attn_args* a, int64_t groups, int64_t nb, int* waves) 
     return brief || (groups * most >= (f32 ? 2048 : 1024) && nb <= (f32 ? 4 : 16) * w && (nb <= 8 || groups * w <= 2048));
 }
 
+// Splits of a prompt launch, by what they cost: a tile takes a lone workgroup
+// 1.25 us (in fp32, whose products bound it, T * D / 1500, and longer where more
+// than two workgroups share a CU, or heads above 128 more than one), a join 3 us
+// and its partial outputs, written and read at 5 TB/s.  Against splits of eight
+// tiles (four in fp32) whatever the outputs' size: 4 rows of 4 new tokens over
+// 2000, 32/8 heads of 128, e4m3 20.7 -> 14.4 us; 300 over 300 22.0 -> 17.5; five
+// prompts of 305, 8/1 heads of 256 24.4 -> 18.4, now whole; in fp32 1000 tokens
+// 145 -> 100, 4 new over 16000 41 -> 59.
+int64_t prompt_splits(const bcg_attn_args* a, int T, int64_t groups, int64_t nb) {
+    const bool f32 = a->q_dtype == BCG_F32;
+    const int dims = a->head_dim <= 64 ? 64 : a->head_dim <= 128 ? 128 : 256;
+    const double tile = f32 ? T * dims / 1500.0 : 1.25;
+    const double join = (double)a->tokens * a->q_heads * a->head_dim * 8 / 5e6;
+    int64_t most = (f32 ? 2 : 1) * kPromptGroups / groups, best = 1;
+    most = most < nb ? most : nb;
+    const int64_t fill = dims == 256 ? 400 : 512;
+    double least = 0.0;
+    for (int64_t s = 1; s <= most && s <= kMaxSplits; ++s) {
+        const double share = f32 && groups * s > fill ? (double)(groups * s) / fill : 1.0;
+        const double us = (double)((nb + s - 1) / s) * tile * share + (s > 1 ? 3.0 + s * join : 0.0);
+        if (s == 1 || us < least) least = us, best = s;
+    }
+    return best;
+}
+
 int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
     clear_error();
     const int rc = check(a, who, prompt);
@@ -145,26 +170,25 @@ int run(const bcg_attn_args* a, const char* who, bool prompt, void* stream) {
         nb = nb < most ? nb : most;
     }
     nb = nb < 1 ? 1 : nb;
-    const int64_t groups = (int64_t)(prompt ? (a->tokens * (int64_t)p.G + C - 1) / C + a->rows : (int64_t)a->rows * p.tiles) * p.kvh;
-    const bool f32 = a->q_dtype == BCG_F32;
-    int64_t aim = kDecodeGroups, least = kMinBlocks;
-    // (in fp32 a prompt's tile takes several times as long: twice as many splits)
-    if (prompt) aim = f32 ? 2 * kPromptGroups : kPromptGroups, least = f32 ? kMinTiles / 2 : kMinTiles;
-    int64_t splits = groups >= aim ? 1 : aim / groups;
-    if (!prompt) {
+    // workgroups of one split: every row's tiles, at most
+    int64_t groups = (int64_t)a->rows * p.tiles;
+    const int64_t full = (a->tokens * (int64_t)p.G + C - 1) / C + a->rows;
+    groups = (prompt && full < groups ? full : groups) * p.kvh;
+    int64_t splits = 1;
+    if (prompt) {
+        splits = prompt_splits(a, T, groups, nb);
+    } else if (!one_launch(a, groups, nb, &p.waves)) {
+        p.waves = 4;
+        splits = groups >= kDecodeGroups ? 1 : kDecodeGroups / groups;
         // half of the aim is enough where the splits would get shorter than 64 blocks
-        const int64_t lng = nb / 64 > aim / 2 / groups ? nb / 64 : aim / 2 / groups;
+        const int64_t lng = nb / 64 > kDecodeGroups / 2 / groups ? nb / 64 : kDecodeGroups / 2 / groups;
         if (splits > lng) splits = lng < 1 ? 1 : lng;
         // and two workgroups a CU where they would get shorter than 16 (8 rows of 4000: 24.7 us,
         // 20.8 with splits of 15 blocks; one of 16000: 21.6, 19.5 with 8)
-        const int64_t few = groups * nb / 512;
-        least = few < least ? least : few < 16 ? few : 16;
-        p.waves = 4;
-        int waves = 0;
-        if (one_launch(a, groups, nb, &waves)) splits = 1, p.waves = waves;
+        const int64_t few = groups * nb / 512, least = few < kMinBlocks ? kMinBlocks : few < 16 ? few : 16;
+        if (splits > kMaxSplits) splits = kMaxSplits;
+        if (splits > (nb + least - 1) / least) splits = (nb + least - 1) / least;
     }
-    if (splits > kMaxSplits) splits = kMaxSplits;
-    if (splits > (nb + least - 1) / least) splits = (nb + least - 1) / least;
     p.chunk = (int)((nb + splits - 1) / splits);
     p.splits = (int)((nb + p.chunk - 1) / p.chunk);
     const int64_t entries = (int64_t)a->tokens * a->q_heads;
