@@ -325,7 +325,7 @@ template <typename QT, int DP, int NW> __device__ __forceinline__ void join_spli
 // 128, bf16, 2.0 GB) 350 us = 5.7 TB/s, where a 2 GiB device copy moves 4.9;
 // 96 rows of up to 8192 in e4m3 (0.72 GB) 145 us = 5.0 TB/s.  One short row
 // (700 tokens, two rows) is a chain of loads (length, table, pages): 6.1 us, and
-// 3.7 us for the join.  Joining in the same launch, by the last workgroup of a
+// 3.4 us for the join.  Joining in the same launch, by the last workgroup of a
 // row, was slower: with fences 866 us instead of 150 (each writes back and drops
 // an L2 that the pages stream through), with device-scope accesses 180.  Heads
 // of 256 in registers for two waves a SIMD: 16 rows of 2000 tokens 67 -> 47 us.
