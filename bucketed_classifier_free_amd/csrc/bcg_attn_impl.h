@@ -339,7 +339,14 @@ __global__ void __launch_bounds__(64 * NW, sizeof(QT) == 2 && (EX || sizeof(KT) 
     const int tile = id % p.tiles; id /= p.tiles;
     const int h = id % p.kvh; id /= p.kvh;
     const int row = id % p.rows, split = id / p.rows;  // short rows' empty splits come last, not every few groups
-    const int len = min(max(p.len[row], 0), p.max_len);
+    int len = min(max(p.len[row], 0), p.max_len), tok = row;
+    if (p.qoff) {
+        // a prompt call of one query a row: the row's first
+        tok = min(max(p.qoff[row], 0), p.tokens);
+        const int n = min(max(p.qoff[row + 1], tok), p.tokens) - tok;
+        if (n == 0) return;
+        len = max(len - n + 1, 0);
+    }
     const int lo = p.window > 0 ? max(0, len - p.window) : 0;
     const BlockList bl = visible_blocks(lo, len, p.sinks, 32);
     const int v0 = split * p.chunk, v1 = min(bl.nb, v0 + p.chunk);
@@ -348,7 +355,7 @@ __global__ void __launch_bounds__(64 * NW, sizeof(QT) == 2 && (EX || sizeof(KT) 
 
     F8 q[S];
     {
-        const QT* qr = static_cast<const QT*>(p.q) + (int64_t)row * p.qstride + (int64_t)(head0 + c) * p.D;
+        const QT* qr = static_cast<const QT*>(p.q) + (int64_t)tok * p.qstride + (int64_t)(head0 + c) * p.D;
 #pragma unroll
         for (int s = 0; s < S; ++s) q[s] = load_q8<QT>(qr, k_dim<KT>(s, g), p.D, c < nh);
     }
@@ -464,7 +471,7 @@ __global__ void __launch_bounds__(64 * NW, sizeof(QT) == 2 && (EX || sizeof(KT) 
     if constexpr (NW == 1) {
         // a wave alone has its columns' outputs in its registers, 4 E dimensions a lane, and its rows are whole
         if (c >= nh) return;
-        const int64_t at = (int64_t)row * p.qh + head0 + c;
+        const int64_t at = (int64_t)tok * p.qh + head0 + c;
         const float inv = l == 0.0f ? 0.0f : (p.vscale ? p.vscale[h] : 1.0f) / l;
         float x[4 * E];
 #pragma unroll
@@ -508,7 +515,7 @@ __global__ void __launch_bounds__(64 * NW, sizeof(QT) == 2 && (EX || sizeof(KT) 
 #pragma unroll
             for (int w = 0; w < NW; ++w) x[j] += o_s[w][hh][d + j];
         }
-        const int64_t at = (int64_t)row * p.qh + head0 + hh;
+        const int64_t at = (int64_t)tok * p.qh + head0 + hh;
         const float vs = p.vscale ? p.vscale[h] : 1.0f;
         if (p.splits == 1) {
             const float inv = sum == 0.0f ? 0.0f : vs / sum;

@@ -298,6 +298,25 @@ def test_prompt_and_decode_agree_with_one_query_a_row():
     check(*decode(c, x), ref, 128, 200, torch.bfloat16)
 
 
+@pytest.mark.parametrize("q,kv", KINDS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 3)])
+@pytest.mark.parametrize("top", [130, 2500])
+def test_prompt_with_at_most_one_query_a_row(q, kv, window, sinks, top):
+    """max_new of 1: rows with a query, without one, with more than it (the
+    first counts), without tokens, and with more queries than tokens."""
+    lens = [top, 40, 0, 77, 1, 2, 200, 16]
+    off = [0, 1, 1, 2, 5, 6, 10, 10, 11]
+    c = make_cache(lens, 2, 64, 16, kv, seed=top)
+    c["table"][0, 2] = -1
+    x = make_queries(13, 6, 64, q, seed=window)
+    ref = reference(x[:11], off, c, 0.125, window, sinks)
+    out, lse = prompt(c, x, off, window, sinks, max_new=1)
+    first = [0, 1, 2, 5, 6, 10]
+    check(out[first], lse[first], tuple(r[first] if isinstance(r, np.ndarray) and r.ndim else r for r in ref), 64, top, TYPES[q])
+    rest = [i for i in range(13) if i not in first]
+    assert torch.isnan(out[rest].float()).all() and torch.isnan(lse[rest]).all()
+
+
 def dense64(x, c, pos, scale, window=0):
     """Attention of x [rows, new, heads, dim] at pos [new], heads == kv_heads,
     in float64 on the GPU; (out, bounds as oracle.decode.attention)."""
